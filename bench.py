@@ -92,6 +92,8 @@ KERNEL_HEADERS = ("combine_shuffling_amd/csrc/move_body.h", "combine_shuffling_a
                   "combine_shuffling_amd/csrc/moe_device.h",
                   "combine_shuffling_amd/csrc/moe_internal.h", "include/moe_shuffle.h")
 KERNEL_UNITS = ("move.hip", "pipeline.hip", "route_plan.hip")
+# Units of the layer's other operators, which no phase timed here launches.
+LAYER_UNITS = ("router.hip", "shuffle_grad.hip", "expert.hip")
 # Kernels that carry no payload rows (plan metadata, counters).
 PLAN_KERNELS = ("route_count_kernel", "route_scan_kernel", "route_assign_kernel",
                 "traffic_clear_kernel", "traffic_kernel", "counters_clear_kernel")
@@ -160,7 +162,7 @@ def unit_kernels():
     for rel in KERNEL_HEADERS:
         in_headers |= set(_KERNEL_DEF.findall(read(rel)))
     units = {}
-    for unit in KERNEL_UNITS:
+    for unit in KERNEL_UNITS + LAYER_UNITS:
         src = read("combine_shuffling_amd/csrc/" + unit)
         units[unit] = set(_KERNEL_DEF.findall(src)) | {
             k for k in in_headers if re.search(r"\b%s\b" % k, src)}

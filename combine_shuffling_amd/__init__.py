@@ -1,7 +1,7 @@
 """MI355X (gfx950) MoE expert-parallel shuffle.
 
-A thin binding over the C ABI of ``libmoeshuffle.so`` (include/moe_shuffle.h):
-the same calls, with torch tensors for device memory and torch's current
+A thin binding over the C ABI of ``libmoeshuffle.so`` (include/moe_shuffle.h and
+include/moe_layer.h): the same calls, with torch tensors for device memory and torch's current
 stream.  Every step of the shuffle runs in the library's HIP kernels; this
 module only checks shapes and passes pointers.
 
@@ -13,6 +13,23 @@ module only checks shapes and passes pointers.
 Banded plans (band_tokens > 0) route each band of consecutive tokens as its
 own batch; ``Plan.pipeline`` runs route, dispatch and combine of every band
 in one persistent launch.
+
+Around the shuffle stand the other operators of a Mixture-of-Experts layer and
+the layer's gradients:
+
+    plan = Plan(T, H, E, k, R)
+    idx, w = router(plan, logits)               # gate logits [T, E] -> ids, combine weights
+    plan.route(idx)
+    recv, _ = dispatch(plan, x)
+    h, pre = expert_linear(plan, recv, w1, activation="swiglu", save_pre=True)
+    y, _ = expert_linear(plan, h, w2)
+    out = combine(plan, y, w)
+
+    grad_y, grad_w = combine_backward(plan, grad_out, y, w)
+    grad_h, grad_w2, _ = expert_linear_backward(plan, grad_y, h, w2)
+    grad_recv, grad_w1, _ = expert_linear_backward(plan, grad_h, recv, w1, pre, "swiglu")
+    grad_x = dispatch_backward(plan, grad_recv)
+    grad_logits = router_backward(plan, logits, idx, grad_w)
 """
 
 from __future__ import annotations
@@ -26,7 +43,8 @@ from . import _abi
 from ._abi import MoeError, ITEM  # noqa: F401
 
 __all__ = ["Plan", "MoeError", "expert_partition", "route_plan", "dispatch", "combine",
-           "dispatch_fp8", "combine_fp8", "combine_hier", "pipeline"]
+           "dispatch_fp8", "combine_fp8", "combine_hier", "pipeline", "router", "router_backward",
+           "expert_linear", "expert_linear_backward", "combine_backward", "dispatch_backward"]
 
 
 def expert_partition(num_experts: int, num_ranks: int) -> list[int]:
@@ -59,6 +77,45 @@ def _need(t: torch.Tensor, shape, dtypes, name: str, device) -> None:
 
 
 _BF16_LIKE = (torch.bfloat16, torch.int16, torch.uint16)
+_BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
+_OUT_CODE = {torch.bfloat16: _abi.OUT_BF16, torch.float32: _abi.OUT_F32}
+
+
+def _out_code(dtype, name: str) -> int:
+    if dtype not in _OUT_CODE:
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32")
+    return _OUT_CODE[dtype]
+
+
+def _out(t: torch.Tensor | None, shape, dtype, name: str, device) -> torch.Tensor:
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, shape, (dtype,), name, device)
+    return t
+
+
+class _On:
+    """Makes `device` the current one where it is not (a kernel is launched on
+    the current device)."""
+
+    def __init__(self, device: torch.device):
+        self.device = device
+        self.prev = None
+
+    def __enter__(self):
+        if self.device.type != "cuda":
+            raise ValueError(f"tensors must be on the GPU, not on {self.device}")
+        now = torch.cuda.current_device()
+        if self.device.index is not None and now != self.device.index:
+            self.prev = now
+            torch.cuda.set_device(self.device)
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            torch.cuda.set_device(self.prev)
+        return False
 
 
 class Plan:
@@ -272,6 +329,178 @@ class Plan:
                    "moe_combine_fp8")
         return out
 
+    # -- moe_router
+    def _router_config(self, score: str, renormalise: bool, nodes_per_token: int, scale: float):
+        if score not in _abi.SCORE:
+            raise ValueError(f"score must be one of {tuple(_abi.SCORE)}")
+        return _abi.RouterConfig(_abi.SCORE[score], int(bool(renormalise)), nodes_per_token, scale)
+
+    def router(self, logits: torch.Tensor, bias: torch.Tensor | None = None,
+               score: str = "softmax", renormalise: bool = True, scale: float = 1.0,
+               nodes_per_token: int = 0, topk_idx: torch.Tensor | None = None,
+               topk_w: torch.Tensor | None = None, stream=None):
+        """Gate logits [T, E] (float32 or bf16) -> (topk_idx int32 [T, k], topk_w float32 [T, k]).
+
+        The k experts of the largest logit + bias (bias: float32 [E], for the choice only), in
+        descending order, ties to the lower id; nodes_per_token m > 0 allows the experts of the
+        token's m best nodes only.  Weights: scale * softmax or sigmoid of the logits, over the
+        sum of the selected ones with renormalise.  The plan need not be routed."""
+        dev = logits.device
+        _need(logits, (self.T, self.E), (torch.float32, torch.bfloat16), "logits", dev)
+        if bias is not None:
+            _need(bias, (self.E,), _F32, "bias", dev)
+        cfg = self._router_config(score, renormalise, nodes_per_token, scale)
+        with _On(dev):
+            topk_idx = _out(topk_idx, (self.T, self.k), torch.int32, "topk_idx", dev)
+            topk_w = _out(topk_w, (self.T, self.k), torch.float32, "topk_w", dev)
+            _abi.check(self._lib.moe_router(self._h, ctypes.byref(cfg), _ptr(logits),
+                                            _OUT_CODE[logits.dtype], _ptr(bias), _ptr(topk_idx),
+                                            _ptr(topk_w), _stream_handle(dev, stream)),
+                       "moe_router")
+        return topk_idx, topk_w
+
+    # -- moe_router_backward
+    def router_backward(self, logits: torch.Tensor, topk_idx: torch.Tensor, grad_w: torch.Tensor,
+                        score: str = "softmax", renormalise: bool = True, scale: float = 1.0,
+                        grad_logits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Gradient of the weights with respect to the logits (the choice fixed): [T, E], every
+        entry written, of the logits' dtype."""
+        dev = logits.device
+        _need(logits, (self.T, self.E), (torch.float32, torch.bfloat16), "logits", dev)
+        _need(topk_idx, (self.T, self.k), (torch.int32,), "topk_idx", dev)
+        _need(grad_w, (self.T, self.k), _F32, "grad_w", dev)
+        cfg = self._router_config(score, renormalise, 0, scale)
+        with _On(dev):
+            grad_logits = _out(grad_logits, (self.T, self.E), logits.dtype, "grad_logits", dev)
+            _abi.check(self._lib.moe_router_backward(
+                self._h, ctypes.byref(cfg), _ptr(logits), _OUT_CODE[logits.dtype], _ptr(topk_idx),
+                _ptr(grad_w), _ptr(grad_logits), _stream_handle(dev, stream)),
+                "moe_router_backward")
+        return grad_logits
+
+    # -- moe_dispatch_backward
+    def dispatch_backward(self, grad_recv: torch.Tensor, grad_x: torch.Tensor | None = None,
+                          out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+        """Gradient of dispatch: grad_x[t] = sum_j grad_recv[slot_of[t, j]], [T, H]."""
+        dev = self.device
+        if dev is None:
+            raise MoeError(_abi.ERR_PLAN_NOT_ROUTED, "dispatch_backward")
+        _need(grad_recv, (self.recv_rows, self.H), _BF16_LIKE, "grad_recv", dev)
+        code = _out_code(out_dtype, "out_dtype")
+        with _On(dev):
+            grad_x = _out(grad_x, (self.T, self.H), out_dtype, "grad_x", dev)
+            _abi.check(self._lib.moe_dispatch_backward(self._h, _ptr(grad_recv), _ptr(grad_x), code,
+                                                       _stream_handle(dev, stream)),
+                       "moe_dispatch_backward")
+        return grad_x
+
+    # -- moe_combine_backward
+    def combine_backward(self, grad_out: torch.Tensor, y: torch.Tensor, topk_w: torch.Tensor,
+                         grad_y: torch.Tensor | None = None, grad_w: torch.Tensor | None = None,
+                         stream=None):
+        """Gradient of combine and combine_hier: returns (grad_y [T*k, H] bf16 in the receive
+        layout, grad_w [T, k] float32); grad_out: [T, H] bf16 or float32."""
+        dev = self.device
+        if dev is None:
+            raise MoeError(_abi.ERR_PLAN_NOT_ROUTED, "combine_backward")
+        _need(grad_out, (self.T, self.H), (torch.float32, torch.bfloat16), "grad_out", dev)
+        _need(y, (self.recv_rows, self.H), _BF16_LIKE, "y", dev)
+        _need(topk_w, (self.T, self.k), _F32, "topk_w", dev)
+        with _On(dev):
+            grad_y = _out(grad_y, (self.recv_rows, self.H), torch.bfloat16, "grad_y", dev)
+            grad_w = _out(grad_w, (self.T, self.k), torch.float32, "grad_w", dev)
+            _abi.check(self._lib.moe_combine_backward(
+                self._h, _ptr(grad_out), _OUT_CODE[grad_out.dtype], _ptr(y), _ptr(topk_w),
+                _ptr(grad_y), _ptr(grad_w), _stream_handle(dev, stream)), "moe_combine_backward")
+        return grad_y, grad_w
+
+    # -- moe_expert_linear
+    def _expert_config(self, w: torch.Tensor, activation: str):
+        """(config, K, N, Z) of a product with weights w [E, Z, K]."""
+        if activation not in _abi.ACTIVATION:
+            raise ValueError(f"activation must be one of {tuple(_abi.ACTIVATION)}")
+        if not isinstance(w, torch.Tensor):
+            raise TypeError("w must be a torch.Tensor")
+        if w.dim() != 3:
+            raise ValueError(f"w has shape {tuple(w.shape)}, expected [experts, out, in]")
+        Z, K = w.shape[1], w.shape[2]
+        N = Z
+        if activation in _abi.GATED:
+            if Z % 2:
+                raise ValueError("a gated activation needs an even number of weight rows")
+            N = Z // 2
+        _need(w, (self.E, Z, K), _BF16, "w", self.device)
+        return _abi.ExpertConfig(K, N, _abi.ACTIVATION[activation]), K, N, Z
+
+    def expert_linear(self, x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
+                      residual: torch.Tensor | None = None, activation: str = "none",
+                      save_pre: bool = False, y: torch.Tensor | None = None,
+                      pre: torch.Tensor | None = None, stream=None):
+        """Every expert's product on its rows of the receive layout: returns (y, pre).
+
+        y[r] = act(x[r] . w[e]^T + bias[e]) + residual[r] for each receive row r of expert e;
+        x [T*k, K], w [E, Z, K], residual and y [T*k, N] bf16, bias [E, Z] float32; Z = 2N (gate
+        rows, then up rows) with "swiglu" and "geglu", else N.  pre: the product before the
+        activation, [T*k, Z] bf16, with save_pre (or a tensor to write), else None."""
+        dev = self.device
+        if dev is None:
+            raise MoeError(_abi.ERR_PLAN_NOT_ROUTED, "expert_linear")
+        cfg, K, N, Z = self._expert_config(w, activation)
+        rows = self.recv_rows
+        _need(x, (rows, K), _BF16, "x", dev)
+        if bias is not None:
+            _need(bias, (self.E, Z), _F32, "bias", dev)
+        if residual is not None:
+            _need(residual, (rows, N), _BF16, "residual", dev)
+        with _On(dev):
+            y = _out(y, (rows, N), torch.bfloat16, "y", dev)
+            if save_pre or pre is not None:
+                pre = _out(pre, (rows, Z), torch.bfloat16, "pre", dev)
+            _abi.check(self._lib.moe_expert_linear(
+                self._h, ctypes.byref(cfg), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(y),
+                _ptr(pre), _stream_handle(dev, stream)), "moe_expert_linear")
+        return y, pre
+
+    # -- moe_expert_linear_backward
+    def expert_linear_backward(self, grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
+                               pre: torch.Tensor | None = None, activation: str = "none",
+                               bias_grad: bool = False, x_grad: bool = True, w_grad: bool = True,
+                               grad_w_dtype: torch.dtype = torch.bfloat16,
+                               workspace: torch.Tensor | None = None, stream=None):
+        """Gradient of expert_linear: returns (grad_x [T*k, K] bf16, grad_w [E, Z, K] of
+        grad_w_dtype, grad_bias [E, Z] float32), None for one that is not wanted.
+
+        pre: what expert_linear stored, needed with an activation.  The gradient of the residual
+        is grad_y."""
+        dev = self.device
+        if dev is None:
+            raise MoeError(_abi.ERR_PLAN_NOT_ROUTED, "expert_linear_backward")
+        cfg, K, N, Z = self._expert_config(w, activation)
+        rows = self.recv_rows
+        _need(grad_y, (rows, N), _BF16, "grad_y", dev)
+        _need(x, (rows, K), _BF16, "x", dev)
+        if activation != "none":
+            if pre is None:
+                raise ValueError("pre is needed with an activation")
+            _need(pre, (rows, Z), _BF16, "pre", dev)
+        else:
+            pre = None
+        code = _out_code(grad_w_dtype, "grad_w_dtype")
+        need = int(self._lib.moe_expert_backward_workspace_bytes(self._h, ctypes.byref(cfg)))
+        if workspace is not None and workspace.numel() * workspace.element_size() < need:
+            raise ValueError("workspace too small")
+        with _On(dev):
+            if workspace is None:
+                workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+            grad_x = torch.empty((rows, K), dtype=torch.bfloat16, device=dev) if x_grad else None
+            grad_w = torch.empty((self.E, Z, K), dtype=grad_w_dtype, device=dev) if w_grad else None
+            grad_b = torch.empty((self.E, Z), dtype=torch.float32, device=dev) if bias_grad else None
+            _abi.check(self._lib.moe_expert_linear_backward(
+                self._h, ctypes.byref(cfg), _ptr(grad_y), _ptr(x), _ptr(w), _ptr(pre), _ptr(grad_x),
+                _ptr(grad_w), code, _ptr(grad_b), _ptr(workspace), _stream_handle(dev, stream)),
+                "moe_expert_linear_backward")
+        return grad_x, grad_w, grad_b
+
     # -- moe_plan_timing / moe_plan_timing_read
     def timing(self, capacity: int) -> None:
         """Time each kernel this plan's calls launch (up to `capacity` launches;
@@ -359,3 +588,46 @@ def pipeline(plan: Plan, topk_idx: torch.Tensor, x: torch.Tensor, topk_w: torch.
              recv=None, out=None, out_dtype: torch.dtype = torch.bfloat16, stream=None):
     """moe_pipeline: returns (recv [T*k, H], out [T, H])."""
     return plan.pipeline(topk_idx, x, topk_w, recv, out, out_dtype, stream=stream)
+
+
+def router(plan: Plan, logits: torch.Tensor, bias=None, score: str = "softmax",
+           renormalise: bool = True, scale: float = 1.0, nodes_per_token: int = 0, topk_idx=None,
+           topk_w=None, stream=None):
+    """moe_router: returns (topk_idx [T, k] int32, topk_w [T, k] float32)."""
+    return plan.router(logits, bias, score, renormalise, scale, nodes_per_token, topk_idx, topk_w,
+                       stream)
+
+
+def router_backward(plan: Plan, logits: torch.Tensor, topk_idx: torch.Tensor, grad_w: torch.Tensor,
+                    score: str = "softmax", renormalise: bool = True, scale: float = 1.0,
+                    grad_logits=None, stream=None) -> torch.Tensor:
+    """moe_router_backward: returns grad_logits [T, E]."""
+    return plan.router_backward(logits, topk_idx, grad_w, score, renormalise, scale, grad_logits,
+                                stream)
+
+
+def dispatch_backward(plan: Plan, grad_recv: torch.Tensor, grad_x=None,
+                      out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """moe_dispatch_backward: returns grad_x [T, H] (bf16 or float32)."""
+    return plan.dispatch_backward(grad_recv, grad_x, out_dtype, stream)
+
+
+def combine_backward(plan: Plan, grad_out: torch.Tensor, y: torch.Tensor, topk_w: torch.Tensor,
+                     grad_y=None, grad_w=None, stream=None):
+    """moe_combine_backward: returns (grad_y [T*k, H] bf16, grad_w [T, k] float32)."""
+    return plan.combine_backward(grad_out, y, topk_w, grad_y, grad_w, stream)
+
+
+def expert_linear(plan: Plan, x: torch.Tensor, w: torch.Tensor, bias=None, residual=None,
+                  activation: str = "none", save_pre: bool = False, y=None, pre=None, stream=None):
+    """moe_expert_linear: returns (y [T*k, N] bf16, pre [T*k, Z] bf16 or None)."""
+    return plan.expert_linear(x, w, bias, residual, activation, save_pre, y, pre, stream)
+
+
+def expert_linear_backward(plan: Plan, grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
+                           pre=None, activation: str = "none", bias_grad: bool = False,
+                           x_grad: bool = True, w_grad: bool = True,
+                           grad_w_dtype: torch.dtype = torch.bfloat16, workspace=None, stream=None):
+    """moe_expert_linear_backward: returns (grad_x, grad_w, grad_bias), None where not wanted."""
+    return plan.expert_linear_backward(grad_y, x, w, pre, activation, bias_grad, x_grad, w_grad,
+                                       grad_w_dtype, workspace, stream)

@@ -1,4 +1,4 @@
-"""ctypes declarations of the C ABI in include/moe_shuffle.h.
+"""ctypes declarations of the C ABI in include/moe_shuffle.h and include/moe_layer.h.
 
 Loads the in-tree libmoeshuffle.so and fails loudly when it is missing: there
 is no fallback of any kind.
@@ -31,6 +31,11 @@ MAX_TOPK = 16
 OUT_BF16 = 0
 OUT_F32 = 1
 
+# moe_layer.h: moe_score, moe_activation
+SCORE = dict(softmax=0, sigmoid=1)
+ACTIVATION = dict(none=0, relu=1, silu=2, gelu=3, swiglu=4, geglu=5)
+GATED = ("swiglu", "geglu")
+
 # moe_item
 ITEM = dict(status=0, counts=1, expert_offsets=2, rank_offsets=3, slot_of=4, row_src=5,
             num_staged=6, stage_offsets=7, stage_of=8, stage_src=9, send_rows=10,
@@ -50,6 +55,24 @@ class MoeConfig(ctypes.Structure):
     ]
 
 
+class RouterConfig(ctypes.Structure):
+    _fields_ = [
+        ("score", ctypes.c_int32),
+        ("renormalise", ctypes.c_int32),
+        ("nodes_per_token", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class ExpertConfig(ctypes.Structure):
+    _fields_ = [
+        ("in_features", ctypes.c_int32),
+        ("out_features", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+    ]
+
+
+# include/moe_shuffle.h
 EXPORTS = (
     "moe_expert_partition", "moe_plan_create", "moe_plan_destroy", "moe_plan_workspace_bytes",
     "moe_plan_recv_rows", "moe_plan_staging_rows_max", "moe_route_plan", "moe_dispatch",
@@ -59,7 +82,13 @@ EXPORTS = (
     "moe_plan_chunk_tokens",
 )
 
-KERNEL_COUNT = 22
+# include/moe_layer.h
+LAYER_EXPORTS = (
+    "moe_router", "moe_router_backward", "moe_dispatch_backward", "moe_combine_backward",
+    "moe_expert_linear", "moe_expert_backward_workspace_bytes", "moe_expert_linear_backward",
+)
+
+KERNEL_COUNT = 31  # moe_kernel and moe_layer_kernel
 
 
 class MoeError(RuntimeError):
@@ -124,6 +153,21 @@ def lib() -> ctypes.CDLL:
     L.moe_plan_timing_read.argtypes = [vp, ctypes.POINTER(i32), ctypes.POINTER(ctypes.c_float),
                                        ctypes.POINTER(ctypes.c_float), i32, ctypes.POINTER(i32)]
     L.moe_plan_timing_read.restype = i32
+    router, expert = ctypes.POINTER(RouterConfig), ctypes.POINTER(ExpertConfig)
+    L.moe_router.argtypes = [vp, router, vp, i32, vp, vp, vp, vp]
+    L.moe_router.restype = i32
+    L.moe_router_backward.argtypes = [vp, router, vp, i32, vp, vp, vp, vp]
+    L.moe_router_backward.restype = i32
+    L.moe_dispatch_backward.argtypes = [vp, vp, vp, i32, vp]
+    L.moe_dispatch_backward.restype = i32
+    L.moe_combine_backward.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp]
+    L.moe_combine_backward.restype = i32
+    L.moe_expert_linear.argtypes = [vp, expert, vp, vp, vp, vp, vp, vp, vp]
+    L.moe_expert_linear.restype = i32
+    L.moe_expert_backward_workspace_bytes.argtypes = [vp, expert]
+    L.moe_expert_backward_workspace_bytes.restype = sz
+    L.moe_expert_linear_backward.argtypes = [vp, expert, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp]
+    L.moe_expert_linear_backward.restype = i32
     L.moe_status_str.argtypes = [i32]
     L.moe_status_str.restype = ctypes.c_char_p
     _lib = L

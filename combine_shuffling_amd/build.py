@@ -6,10 +6,12 @@ Cross-compiles with hipcc; no GPU is needed to build.
 
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,7 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmoeshuffle.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
-SOURCES = ("route_plan.hip", "move.hip", "pipeline.hip", "moe_api.cpp")
+SOURCES = ("route_plan.hip", "move.hip", "pipeline.hip", "router.hip", "shuffle_grad.hip", "expert.hip",
+           "moe_api.cpp", "moe_layer_api.cpp")
 
 # -packed-fp32-ops: no packed fp32 instructions in device code.
 HIP_FLAGS = [
@@ -34,16 +37,7 @@ def hipcc() -> str:
     return path
 
 
-def build(verbose: bool = False, extra_flags=(), out: str | None = None) -> str:
-    """Compile every source into ``out`` (default LIB_PATH; always recompiles).
-
-    extra_flags: more hipcc flags (for instance -save-temps to keep the
-    gfx950 assembly).
-    """
-    out = LIB_PATH if out is None else out
-    tmp = out + ".tmp"
-    cmd = [hipcc(), *HIP_FLAGS, *extra_flags, f"-I{INCLUDE}", f"-I{CSRC}",
-           *[os.path.join(CSRC, s) for s in SOURCES], "-o", tmp]
+def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -53,6 +47,25 @@ def build(verbose: bool = False, extra_flags=(), out: str | None = None) -> str:
         raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
     if verbose and msgs:
         print("\n".join(msgs))
+
+
+def build(verbose: bool = False, extra_flags=(), out: str | None = None) -> str:
+    """Compile every source into ``out`` (default LIB_PATH; always recompiles).
+
+    extra_flags: more hipcc flags (for instance -save-temps to keep the
+    gfx950 assembly).
+    """
+    out = LIB_PATH if out is None else out
+    tmp = out + ".tmp"
+    compile_flags = [f for f in HIP_FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory() as objs:
+        pairs = [(os.path.join(CSRC, s), os.path.join(objs, s + ".o")) for s in SOURCES]
+        cmds = [[hipcc(), *compile_flags, *extra_flags, f"-I{INCLUDE}", f"-I{CSRC}", "-c", src, "-o", obj]
+                for src, obj in pairs]
+        with concurrent.futures.ThreadPoolExecutor(max_workers=4) as pool:
+            list(pool.map(lambda c: _run(c, verbose), cmds))
+        _run([hipcc(), "--offload-arch=gfx950", "-fPIC", "-shared", *[o for _, o in pairs], "-o", tmp],
+             verbose)
     os.replace(tmp, out)
     return out
 

@@ -10,51 +10,13 @@
 #include <new>
 #include <vector>
 
-#include "moe_internal.h"
-
-namespace moe {
-// Event pairs of moe_plan_timing and the kernel of each recorded launch.
-struct LaunchTimer {
-  std::vector<hipEvent_t> start, stop;
-  std::vector<int32_t> ids;
-  int used = 0;
-};
-}  // namespace moe
-
-struct moe_plan {
-  moe_config cfg;
-  moe::Dims d;
-  moe::Layout layout;
-  int64_t staging_rows_max;
-  // Bound by moe_route_plan.
-  const int32_t* idx;
-  void* ws;
-  moe::Work work;
-  bool routed;     // route_count has been launched for the bound routing
-  bool scanned;    // route_scan has been launched for it (tile bases, offsets, status)
-  bool assigned;   // slot_of / row_src (and stage_of / stage_src) are final
-  moe::LaunchTimer* timer;  // per-launch timing, or null
-};
+#include "moe_layer.h"
+#include "moe_plan.h"
 
 namespace moe {
 namespace {
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-moe_status from_hip(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
-
-// The timer of the plan whose call is running on this thread.
-thread_local LaunchTimer* tl_timer = nullptr;
-
-// Makes `plan`'s timer the active one for the lifetime of the scope (each
-// API call that launches kernels opens one).
-struct TimerScope {
-  LaunchTimer* prev;
-  explicit TimerScope(const moe_plan* plan) : prev(tl_timer) { tl_timer = plan->timer; }
-  ~TimerScope() { tl_timer = prev; }
-};
 
 void destroy_events(LaunchTimer* t) {
   for (hipEvent_t e : t->start) (void)hipEventDestroy(e);
@@ -66,6 +28,8 @@ void destroy_events(LaunchTimer* t) {
 }
 
 }  // namespace
+
+thread_local LaunchTimer* tl_timer = nullptr;
 
 bool timer_take(int id, hipEvent_t* start, hipEvent_t* stop) {
   LaunchTimer* t = tl_timer;
@@ -145,7 +109,6 @@ Work bind_work(const Layout& l, void* base) {
   return w;
 }
 
-// Launches the plan's scan if the route left it to the gather (small plans).
 moe_status ensure_scanned(moe_plan* plan, hipStream_t s) {
   if (plan->scanned) return MOE_OK;
   if (launch_route_scan(plan->d, plan->work, s) != hipSuccess) return MOE_ERR_HIP;
@@ -153,8 +116,6 @@ moe_status ensure_scanned(moe_plan* plan, hipStream_t s) {
   return MOE_OK;
 }
 
-// Makes slot_of / row_src (and the staging arrays) final when no dispatch
-// has done it since the last route.
 moe_status ensure_assigned(moe_plan* plan, hipStream_t s) {
   if (plan->assigned) return MOE_OK;
   if (ensure_scanned(plan, s) != MOE_OK) return MOE_ERR_HIP;
@@ -291,7 +252,7 @@ void moe_plan_destroy(moe_plan* plan) {
 }
 
 const char* moe_kernel_name(int32_t kernel) {
-  static const char* const names[MOE_KERNEL_COUNT] = {
+  static const char* const names[MOE_LAYER_KERNEL_END] = {
       "route_count_kernel",   "route_scan_kernel",      "route_assign_kernel",
       "traffic_clear_kernel", "traffic_kernel",         "gather_kernel",
       "gather_scan_kernel",   "stage_a_kernel",         "stage_b_kernel",
@@ -299,8 +260,11 @@ const char* moe_kernel_name(int32_t kernel) {
       "gather_fp8_kernel",    "gather_fp8_scan_kernel", "stage_a_fp8_kernel",
       "stage_b_fp8_kernel",   "combine_fp8_kernel",     "pipeline_kernel",
       "counters_clear_kernel", "stage_ab_kernel",       "stage_ab_fp8_kernel",
-      "combine_pn_kernel"};
-  return kernel >= 0 && kernel < MOE_KERNEL_COUNT ? names[kernel] : "?";
+      "combine_pn_kernel",
+      "router_kernel",        "router_grad_kernel",     "dispatch_grad_kernel",
+      "combine_grad_kernel",  "expert_rows_kernel",     "expert_rows_grad_kernel",
+      "expert_wgrad_kernel",  "expert_act_grad_kernel", "expert_bias_sum_kernel"};
+  return kernel >= 0 && kernel < MOE_LAYER_KERNEL_END ? names[kernel] : "?";
 }
 
 moe_status moe_plan_timing(moe_plan* plan, int32_t capacity) {
