@@ -45,23 +45,18 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 #define MOE_LDS __attribute__((address_space(3)))
 
-constexpr int kBK = 64;                   // contraction step: 128 bytes of bf16
+constexpr int kBK = 32;                   // contraction step: 64 bytes of bf16
 constexpr int kBufferFormat = 0x00020000; // raw buffer descriptor, word 3 (gfx9 family)
 constexpr uint32_t kPast = 0x80000000u;   // an offset past every descriptor's end
 constexpr int kXcds = 8;
 constexpr int64_t kMaxTileBlocks = (int64_t)1 << 22;  // blocks a launch (work-items are counted in 32 bits)
 
-__device__ __forceinline__ uint32_t bf16_bits(float f) {
-  const uint32_t u = __float_as_uint(f);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return ((u >> 16) | 0x40u) & 0xffffu;
-  return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
-}
-
+// Two floats to bf16, round to nearest even, NaN stays NaN (one instruction).
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  return bf16_bits(lo) | bf16_bits(hi) << 16;
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
-
-__device__ __forceinline__ float bf16_value(uint32_t bits) { return __uint_as_float(bits << 16); }
 
 __device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8]) {
 #pragma unroll
@@ -96,28 +91,66 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_buffer(const char* p, 
 
 __device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(-0.70710678118654752f * z); }
 
-__device__ __forceinline__ float act_value(int act, float z) {
+__device__ __forceinline__ float logistic(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
+
+// z := act(z), one choice for eight values.
+__device__ __forceinline__ void act_values(int act, float (&z)[8]) {
   switch (act) {
-    case MOE_ACT_RELU: return z > 0.0f ? z : z != z ? z : 0.0f;
+    case MOE_ACT_RELU:
+#pragma unroll
+      for (int q = 0; q < 8; ++q) z[q] = z[q] < 0.0f ? 0.0f : z[q];
+      break;
     case MOE_ACT_SILU:
-    case MOE_ACT_SWIGLU: return z / (1.0f + __expf(-z));
+    case MOE_ACT_SWIGLU:
+#pragma unroll
+      for (int q = 0; q < 8; ++q) z[q] *= logistic(z[q]);
+      break;
     case MOE_ACT_GELU:
-    case MOE_ACT_GEGLU: return z * normal_cdf(z);
-    default: return z;
+    case MOE_ACT_GEGLU:
+#pragma unroll
+      for (int q = 0; q < 8; ++q) z[q] *= normal_cdf(z[q]);
+      break;
+    default: break;
   }
 }
 
-__device__ __forceinline__ float act_slope(int act, float z) {
+// value := act(z), slope := act'(z).
+__device__ __forceinline__ void act_slopes(int act, const float (&z)[8], float (&value)[8],
+                                           float (&slope)[8]) {
   switch (act) {
-    case MOE_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
+    case MOE_ACT_RELU:
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        slope[q] = z[q] > 0.0f ? 1.0f : 0.0f;
+        value[q] = z[q] < 0.0f ? 0.0f : z[q];
+      }
+      break;
     case MOE_ACT_SILU:
-    case MOE_ACT_SWIGLU: {
-      const float q = 1.0f / (1.0f + __expf(-z));
-      return q * (1.0f + z * (1.0f - q));
-    }
+    case MOE_ACT_SWIGLU:
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float p = logistic(z[q]);
+        value[q] = z[q] * p;
+        slope[q] = p * (1.0f + z[q] * (1.0f - p));
+      }
+      break;
     case MOE_ACT_GELU:
-    case MOE_ACT_GEGLU: return normal_cdf(z) + z * 0.3989422804014327f * __expf(-0.5f * z * z);
-    default: return 1.0f;
+    case MOE_ACT_GEGLU:
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float p = normal_cdf(z[q]);
+        value[q] = z[q] * p;
+        slope[q] = p + z[q] * 0.3989422804014327f * __expf(-0.5f * z[q] * z[q]);
+      }
+      break;
+    default:
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        value[q] = z[q];
+        slope[q] = 1.0f;
+      }
   }
 }
 
@@ -153,14 +186,47 @@ __device__ __forceinline__ Segment find_segment(const int32_t* off, int E, int s
   return s;
 }
 
-// Consecutive tiles go to the same XCD (blocks are dealt to the XCDs in
-// turn), so that tiles sharing an operand find it in that XCD's L2.
-__device__ __forceinline__ int64_t tile_of_block(int64_t base, int64_t total) {
-  const int64_t n = min((int64_t)gridDim.x, total - base);
-  const int64_t per = (n + kXcds - 1) / kXcds;
-  const int64_t t = (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
-  return blockIdx.x / kXcds < per && t < n ? base + t : total;
-}
+// Which tile of a [mtiles, ntiles] grid (or of a row of such grids, one an
+// expert) a block computes.  The tiles are cut into groups of about kGroup x
+// kGroup result elements, and the groups are dealt to the XCDs in turn (as the hardware deals
+// the blocks): the blocks that run on an XCD at one time share few rows and
+// columns of the operands, which they find in that XCD's L2, and neighbouring
+// groups run on the other XCDs, which find them in the cache behind it.
+struct Tile {
+  int grid, m, n;
+  bool live;
+};
+
+constexpr int kGroup = 1024;
+
+template <int BM, int BN>
+struct TileGrid {
+  static constexpr int kGroupM = kGroup / BM, kGroupN = kGroup / BN, kTiles = kGroupM * kGroupN;
+  int grids, mtiles, ntiles;
+  int mgroups, ngroups;
+
+  TileGrid(int grids_, int mtiles_, int ntiles_)
+      : grids(grids_), mtiles(mtiles_), ntiles(ntiles_),
+        mgroups((mtiles_ + kGroupM - 1) / kGroupM), ngroups((ntiles_ + kGroupN - 1) / kGroupN) {}
+  // Blocks of all launches together.
+  int64_t blocks() const {
+    const int64_t groups = (int64_t)grids * mgroups * ngroups;
+    return (groups + kXcds - 1) / kXcds * kXcds * kTiles;
+  }
+  __device__ __forceinline__ Tile at(int64_t block) const {
+    const int64_t i = block / kXcds;
+    const int64_t group = i / kTiles * kXcds + block % kXcds;
+    const int in = (int)(i % kTiles);
+    const int per = mgroups * ngroups;
+    Tile t;
+    t.grid = (int)(group / per);
+    const int g = (int)(group % per);
+    t.m = g / ngroups * kGroupM + in / kGroupN;
+    t.n = g % ngroups * kGroupN + in % kGroupN;
+    t.live = t.grid < grids && t.m < mtiles && t.n < ntiles;
+    return t;
+  }
+};
 
 // ---- the tile product
 
@@ -179,23 +245,20 @@ struct TileProduct {
   static constexpr int TM = BM / WM, TN = BN / WN, MI = TM / 16, NJ = TN / 16;
   static constexpr int kABytes = BM * kBK * 2, kBBytes = BN * kBK * 2;
   static constexpr int kStage = kABytes + kBBytes;
-  static constexpr int kLds = 2 * kStage;
+  static constexpr int kStages = 3;
+  static constexpr int kLds = kStages * kStage;
   static constexpr int QA = kABytes / 1024 / kNW, QB = kBBytes / 1024 / kNW;  // loads a wave and stage
   static_assert(QA * kNW * 1024 == kABytes && QB * kNW * 1024 == kBBytes);
   static_assert(BT || TN == 64, "the permuted columns of a wave are 64 wide");
 
-  // Byte offset of a lane's 16 bytes for the wave's q-th load of a stage.
-  // Contiguous contraction: LDS row r (128 bytes) holds chunk p ^ swizzle(r)
-  // at position p.
-  template <bool B>
-  static __device__ __forceinline__ int row_of_load(int wave, int lane, int q) {
-    return (q * kNW + wave) * 8 + lane / 8;
-  }
-  // A's rows are read in order; B's in the order of the permuted columns, so
-  // each has the swizzle that spreads its own reads.
+  // Contiguous contraction: LDS row r (64 bytes, 4 chunks) holds chunk
+  // p ^ swizzle(r) at position p.  A's rows are read in order; B's in the
+  // order of the permuted columns (rows i % 4 + 16 * (i / 4) for lane i), so
+  // each has the swizzle that spreads its own eight consecutive lanes over
+  // all banks.
   template <bool B>
   static __device__ __forceinline__ int swizzle(int r) {
-    return B ? (r & 3) | ((r >> 4) & 1) << 2 : r & 7;
+    return B ? ((r >> 1) & 1) | ((r >> 4) & 1) << 1 : (r >> 1) & 3;
   }
   // Transposed: LDS row kr (along the contraction) of W columns; the 32-byte
   // block b of a row sits at position b ^ spread(kr).
@@ -203,6 +266,7 @@ struct TileProduct {
   static __device__ __forceinline__ int spread(int kr) {
     return ((kr & 3) | ((kr >> 3) & 3) << 2) & (W / 16 - 1);
   }
+  // Byte offset in memory of a lane's 16 bytes for the wave's q-th load.
   template <int W>
   static __device__ __forceinline__ uint32_t offset_t(uint32_t ld, int wave, int lane, int q) {
     constexpr int per = W / 8;       // 16-byte positions a row
@@ -220,6 +284,10 @@ struct TileProduct {
     return slab * 32 + q * 8 + (jj & 1) * 4 + (r & 3) + (jj >> 1) * gate_up;
   }
 
+  struct Fragments {
+    bf16x8 a[MI], b[NJ];
+  };
+
   f32x4 acc[MI][NJ];
 
   __device__ __forceinline__ void clear() {
@@ -229,50 +297,122 @@ struct TileProduct {
       for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  // acc += A B over `len` contraction elements.  gate_up: memory rows from the
-  // gate's to the up projection's row (gated only).
-  __device__ __forceinline__ void run(const Operand& a, const Operand& b, int len, int gate_up,
-                                      char* lds) {
+  // acc += A B over `len` contraction elements.  rows: result rows that are
+  // wanted (the others' products are skipped, 16 rows at a time).  gate_up:
+  // memory rows from the gate's to the up projection's row (gated only).
+  //
+  // While the fragments of step s (in registers) are multiplied, those of
+  // step s + 1 are read from LDS and the loads of steps s + 2 and s + 3 are
+  // under way.  One barrier a step: before it a wave waits for its own
+  // fragments of step s (so stage s is free after it, for step s + 3) and for
+  // its own loads of step s + 1 (so they can be read after it).  Steps past
+  // the end load zeros through empty descriptors, which keeps the number of
+  // loads under way the same in every step.
+  __device__ __forceinline__ void run(const Operand& a, const Operand& b, int len, int rows,
+                                      int gate_up, char* lds) {
+    const int m0 = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) / WN * TM;
+    const int used = min(max((rows - m0 + 15) / 16, 0), MI);
+    if (used == MI)
+      sweep<true>(a, b, len, MI, gate_up, lds);
+    else
+      sweep<false>(a, b, len, used, gate_up, lds);
+  }
+
+  template <bool FULL>
+  __device__ __forceinline__ void sweep(const Operand& a, const Operand& b, int len, int used,
+                                        int gate_up, char* lds) {
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     uint32_t va[QA], vb[QB];
     int ca[QA], cb[QB];  // chunk of the step a lane loads (contiguous contraction)
 #pragma unroll
     for (int q = 0; q < QA; ++q) {
-      if constexpr (AT) {
-        va[q] = offset_t<BM>(a.ld, wave, lane, q);
-        ca[q] = 0;
-      } else {
-        const int r = row_of_load<false>(wave, lane, q);
-        ca[q] = (lane & 7) ^ swizzle<false>(r);
-        va[q] = (uint32_t)r * a.ld + ca[q] * 16;
-      }
+      const int r = (q * kNW + wave) * 16 + lane / 4;
+      ca[q] = AT ? 0 : (lane & 3) ^ swizzle<false>(r);
+      va[q] = AT ? offset_t<BM>(a.ld, wave, lane, q) : (uint32_t)r * a.ld + ca[q] * 16;
     }
 #pragma unroll
     for (int q = 0; q < QB; ++q) {
-      if constexpr (BT) {
-        vb[q] = offset_t<BN>(b.ld, wave, lane, q);
-        cb[q] = 0;
-      } else {
-        const int r = row_of_load<true>(wave, lane, q);
-        cb[q] = (lane & 7) ^ swizzle<true>(r);
-        vb[q] = (uint32_t)b_row(r, gate_up) * b.ld + cb[q] * 16;
-      }
+      const int r = (q * kNW + wave) * 16 + lane / 4;
+      cb[q] = BT ? 0 : (lane & 3) ^ swizzle<true>(r);
+      vb[q] = BT ? offset_t<BN>(b.ld, wave, lane, q)
+                 : (uint32_t)b_row(r, gate_up) * b.ld + cb[q] * 16;
     }
+    const int m0 = wave / WN * TM, n0 = wave % WN * TN;
     const int steps = (len + kBK - 1) / kBK;
-    auto load = [&](int step) {
-      char* at = lds + (step & 1) * kStage + wave * 1024;
+    auto load = [&](int step, char* to) {
       const int done = step * kBK, left = len - done;
-      issue<AT, QA>(a, va, ca, done, left, at);
-      issue<BT, QB>(b, vb, cb, done, left, at + kABytes);
+      issue<AT, QA>(a, va, ca, done, left, to + wave * 1024);
+      issue<BT, QB>(b, vb, cb, done, left, to + kABytes + wave * 1024);
     };
-    if (steps > 0) load(0);
-    for (int s = 0; s < steps; ++s) {
-      __syncthreads();  // this step's loads have landed; the other stage is free
-      if (s + 1 < steps) load(s + 1);
-      multiply(lds + (s & 1) * kStage, wave, lane);
+    auto read = [&](Fragments& f, const char* from) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) f.b[j] = fragment<BT, true, BN>(from + kABytes, n0, j, lane);
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+        if (FULL || i < used) f.a[i] = fragment<AT, false, BM>(from, m0, i, lane);
+    };
+    int put = 0, get = kStage;  // LDS offsets of the next stage to load and to read
+    auto step = [&](int s, const Fragments& now, Fragments& next) {
+      wait_and_meet<QA + QB>();
+      refill(load, read, s + 3, next, lds + put, lds + get);
+      put = put == (kStages - 1) * kStage ? 0 : put + kStage;
+      get = get == (kStages - 1) * kStage ? 0 : get + kStage;
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+        if (FULL || i < used)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now.b[j], now.a[i], acc[i][j], 0, 0, 0);
+      if constexpr (FULL) interleave();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    load(0, lds);
+    load(1, lds + kStage);
+    load(2, lds + 2 * kStage);
+    wait_and_meet<2 * (QA + QB)>();
+    Fragments f0{}, f1{};
+    read(f0, lds);
+    for (int s = 0; s < steps; s += 2) {
+      step(s, f0, f1);
+      if (s + 1 < steps) step(s + 1, f1, f0);
     }
-    __syncthreads();
+    wait_and_meet<0>();  // nothing may land in LDS after the block has ended
+  }
+
+  // The loads of a later step and the reads of the next.  The two stages are
+  // different ones, and saying so (restrict) matters: where the compiler sees
+  // that a read from LDS may touch what a load to LDS writes, it waits for
+  // every load under way before the read.
+  template <typename L, typename R>
+  static __device__ __forceinline__ void refill(const L& load, const R& read, int step,
+                                                Fragments& next, char* __restrict__ to,
+                                                const char* __restrict__ from) {
+    load(step, to);
+    read(next, from);
+  }
+
+  // Waits until at most N of this wave's loads to LDS and none of its LDS
+  // reads are under way, then for the block's other waves.
+  template <int N>
+  static __device__ __forceinline__ void wait_and_meet() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // Asks the scheduler to start with products (whose fragments have been
+  // waited for) and to spread the loads and the reads over the rest.
+  static __device__ __forceinline__ void interleave() {
+    constexpr int loads = QA + QB, reads = MI * (AT ? 2 : 1) + NJ * (BT ? 2 : 1);
+    constexpr int products = MI * NJ, each = (products - 2) / reads;
+    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);  // matrix instructions
+#pragma unroll
+    for (int i = 0; i < reads; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
+      if (i < loads) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);  // load
+      __builtin_amdgcn_sched_group_barrier(0x008, each, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, products - 2 - reads * each, 0);
   }
 
   template <bool T, int Q>
@@ -282,11 +422,11 @@ struct TileProduct {
     uint32_t bytes;
     if constexpr (T) {
       base = o.base + (int64_t)done * o.ld;
-      bytes = (uint32_t)min(left, kBK) * o.ld;
-      bytes = bytes > o.bytes ? bytes - o.bytes : 0;  // bytes: the tile's first column
+      bytes = (uint32_t)max(min(left, kBK), 0) * o.ld;
+      bytes = bytes > o.bytes ? bytes - o.bytes : 0;  // o.bytes: the tile's first column
     } else {
       base = o.base + (int64_t)done * 2;
-      bytes = o.bytes > (uint32_t)done * 2 ? o.bytes - done * 2 : 0;
+      bytes = left > 0 && o.bytes > (uint32_t)done * 2 ? o.bytes - done * 2 : 0;
     }
     const __amdgpu_buffer_rsrc_t r = uniform_buffer(base, bytes);
 #pragma unroll
@@ -300,37 +440,18 @@ struct TileProduct {
   }
 
   template <bool T, bool B, int W>
-  static __device__ __forceinline__ bf16x8 fragment(const char* tile, int first, int f, int kk,
-                                                    int lane) {
+  static __device__ __forceinline__ bf16x8 fragment(const char* tile, int first, int f, int lane) {
     const int i = lane & 15, g = lane >> 4;
     if constexpr (T) {
-      const int kr = kk * 32 + g * 8 + (i >> 2);
+      const int kr = g * 8 + (i >> 2);
       const char* p = tile + kr * (W * 2) + (((first / 16 + f) ^ spread<W>(kr)) << 5) + (i & 3) * 8;
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)p);
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(p + 4 * W * 2));
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
       const int r = B ? first + (i >> 2) * 16 + f * 4 + (i & 3) : first + f * 16 + i;
-      const char* p = tile + r * 128 + (((kk * 4 + g) ^ swizzle<B>(r)) << 4);
+      const char* p = tile + r * 64 + ((g ^ swizzle<B>(r)) << 4);
       return *reinterpret_cast<const bf16x8*>(p);
-    }
-  }
-
-  __device__ __forceinline__ void multiply(const char* stage, int wave, int lane) {
-    const int m0 = wave / WN * TM, n0 = wave % WN * TN;
-#pragma unroll
-    for (int kk = 0; kk < kBK / 32; ++kk) {
-      bf16x8 fb[NJ], fa[MI];
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        fb[j] = fragment<BT, true, BN>(stage + kABytes, n0, j, kk, lane);
-#pragma unroll
-      for (int i = 0; i < MI; ++i) fa[i] = fragment<AT, false, BM>(stage, m0, i, kk, lane);
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
     }
   }
 };
@@ -344,24 +465,24 @@ struct TileProduct {
 // ---- rows: y = act(x w^T + bias) + residual
 
 template <typename P>
-__global__ __launch_bounds__(P::kThreads) void expert_rows_kernel(
+__global__ __launch_bounds__(P::kThreads, 2) void expert_rows_kernel(
     ExpertDims x, const int32_t* __restrict__ off, const char* __restrict__ a,
     const char* __restrict__ w, const float* __restrict__ bias,
     const uint16_t* __restrict__ residual, uint16_t* __restrict__ y, uint16_t* __restrict__ pre,
-    int64_t base, int64_t total, int ntiles) {
+    TileGrid<P::BM, P::BN> grid, int64_t base) {
   __shared__ __align__(1024) char lds[P::kLds];
   constexpr int kCols = P::GATED ? P::BN / 2 : P::BN;  // columns of y a tile
-  const int64_t tile = tile_of_block(base, total);
-  if (tile >= total) return;
-  const Segment s = find_segment(off, x.E, (int)(tile / ntiles), P::BM);
+  const Tile tile = grid.at(base + blockIdx.x);
+  if (!tile.live) return;
+  const Segment s = find_segment(off, x.E, tile.m, P::BM);
   if (s.rows <= 0) return;
-  const int n0 = (int)(tile % ntiles) * kCols;
+  const int n0 = tile.n * kCols;
   const uint32_t ld = (uint32_t)x.K * 2;
   Operand oa{a + (int64_t)s.row * ld, ld, (uint32_t)s.rows * ld};
   Operand ob{w + ((int64_t)s.e * x.Z + n0) * ld, ld, (uint32_t)(x.Z - n0) * ld};
   P p;
   p.clear();
-  p.run(oa, ob, x.K, x.N, lds);
+  p.run(oa, ob, x.K, s.rows, x.N, lds);
 
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int g = lane >> 4;
@@ -401,10 +522,12 @@ __global__ __launch_bounds__(P::kThreads) void expert_rows_kernel(
       float gate[8], up[8], out[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        gate[q] = z[q];
+        out[q] = gate[q] = z[q];
         up[q] = z[8 + q];
-        out[q] = act_value(x.act, gate[q]) * up[q];
       }
+      act_values(x.act, out);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) out[q] *= up[q];
       if (pre != nullptr) {
         *reinterpret_cast<u32x4*>(pre + row * x.Z + c0) = pack8(gate);
         *reinterpret_cast<u32x4*>(pre + row * x.Z + x.N + c0) = pack8(up);
@@ -425,8 +548,7 @@ __global__ __launch_bounds__(P::kThreads) void expert_rows_kernel(
 #pragma unroll
         for (int q = 0; q < 8; ++q) out[q] = z[h * 8 + q];
         if (pre != nullptr) *reinterpret_cast<u32x4*>(pre + row * x.Z + col) = pack8(out);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) out[q] = act_value(x.act, out[q]);
+        act_values(x.act, out);
         if (residual != nullptr) {
           float r[8];
           unpack8(*reinterpret_cast<const u32x4*>(residual + row * x.N + col), r);
@@ -442,21 +564,21 @@ __global__ __launch_bounds__(P::kThreads) void expert_rows_kernel(
 // ---- rows grad: gx = gz w
 
 template <typename P>
-__global__ __launch_bounds__(P::kThreads) void expert_rows_grad_kernel(
+__global__ __launch_bounds__(P::kThreads, 2) void expert_rows_grad_kernel(
     ExpertDims x, const int32_t* __restrict__ off, const char* __restrict__ gz,
-    const char* __restrict__ w, uint16_t* __restrict__ gx, int64_t base, int64_t total, int ntiles) {
+    const char* __restrict__ w, uint16_t* __restrict__ gx, TileGrid<P::BM, P::BN> grid, int64_t base) {
   __shared__ __align__(1024) char lds[P::kLds];
-  const int64_t tile = tile_of_block(base, total);
-  if (tile >= total) return;
-  const Segment s = find_segment(off, x.E, (int)(tile / ntiles), P::BM);
+  const Tile tile = grid.at(base + blockIdx.x);
+  if (!tile.live) return;
+  const Segment s = find_segment(off, x.E, tile.m, P::BM);
   if (s.rows <= 0) return;
-  const int n0 = (int)(tile % ntiles) * P::BN;
+  const int n0 = tile.n * P::BN;
   const uint32_t lda = (uint32_t)x.Z * 2, ldb = (uint32_t)x.K * 2;
   Operand oa{gz + (int64_t)s.row * lda, lda, (uint32_t)s.rows * lda};
   Operand ob{w + (int64_t)s.e * x.Z * ldb + n0 * 2, ldb, (uint32_t)n0 * 2};
   P p;
   p.clear();
-  p.run(oa, ob, x.Z, 0, lds);
+  p.run(oa, ob, x.Z, s.rows, 0, lds);
 
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int m0 = wave / P::WN * P::TM + (lane & 15);
@@ -479,23 +601,20 @@ __global__ __launch_bounds__(P::kThreads) void expert_rows_grad_kernel(
 // ---- wgrad: gw[e] = gz^T x
 
 template <typename P, bool F32>
-__global__ __launch_bounds__(P::kThreads) void expert_wgrad_kernel(
+__global__ __launch_bounds__(P::kThreads, 2) void expert_wgrad_kernel(
     ExpertDims x, const int32_t* __restrict__ off, const char* __restrict__ gz,
-    const char* __restrict__ a, void* __restrict__ gw, int64_t base, int64_t total, int mtiles,
-    int ntiles) {
+    const char* __restrict__ a, void* __restrict__ gw, TileGrid<P::BM, P::BN> grid, int64_t base) {
   __shared__ __align__(1024) char lds[P::kLds];
-  const int64_t tile = tile_of_block(base, total);
-  if (tile >= total) return;
-  const int e = (int)(tile / ((int64_t)mtiles * ntiles));
-  const int in = (int)(tile % ((int64_t)mtiles * ntiles));
-  const int z0 = in / ntiles * P::BM, n0 = in % ntiles * P::BN;
+  const Tile tile = grid.at(base + blockIdx.x);
+  if (!tile.live) return;
+  const int e = tile.grid, z0 = tile.m * P::BM, n0 = tile.n * P::BN;
   const int o0 = x.rows > 0 ? off[e] : 0, rows = x.rows > 0 ? off[e + 1] - o0 : 0;
   const uint32_t lda = (uint32_t)x.Z * 2, ldb = (uint32_t)x.K * 2;
   Operand oa{gz + (int64_t)o0 * lda + z0 * 2, lda, (uint32_t)z0 * 2};
   Operand ob{a + (int64_t)o0 * ldb + n0 * 2, ldb, (uint32_t)n0 * 2};
   P p;
   p.clear();
-  p.run(oa, ob, rows, 0, lds);
+  p.run(oa, ob, rows, x.Z - z0, 0, lds);
 
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int m0 = z0 + wave / P::WN * P::TM + (lane & 15);
@@ -556,15 +675,17 @@ __global__ __launch_bounds__(kActCols * kActRows) void expert_act_grad_kernel(
         for (int q = 0; q < 8; ++q) o[q] = g[q];
       } else {
         unpack8(*reinterpret_cast<const u32x4*>(pre + row * x.Z + col), z);
+        float value[8], slope[8];
+        act_slopes(x.act, z, value, slope);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) o[q] = g[q] * act_slope(x.act, z[q]);
+        for (int q = 0; q < 8; ++q) o[q] = g[q] * slope[q];
         if (two) {
           float up[8], u[8];
           unpack8(*reinterpret_cast<const u32x4*>(pre + row * x.Z + x.N + col), up);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             o[q] *= up[q];
-            u[q] = g[q] * act_value(x.act, z[q]);
+            u[q] = g[q] * value[q];
             sum[1][q] += u[q];
           }
           if (gz != nullptr) *reinterpret_cast<u32x4*>(gz + row * x.Z + x.N + col) = pack8(u);
@@ -603,14 +724,13 @@ __global__ __launch_bounds__(256) void expert_bias_sum_kernel(ExpertDims x,
   gb[(int64_t)e * x.Z + n] = t;
 }
 
-// Launches `total` tiles in ranges of at most kMaxTileBlocks blocks.
+// Launches `total` blocks in ranges of at most kMaxTileBlocks (a multiple of
+// the XCDs, so that a block keeps its XCD).
 template <typename F>
 hipError_t in_ranges(int64_t total, F f) {
   hipError_t e = hipSuccess;
-  for (int64_t b = 0; b < total && e == hipSuccess; b += kMaxTileBlocks) {
-    const int64_t n = std::min(total - b, kMaxTileBlocks);
-    e = f(dim3((uint32_t)((n + kXcds - 1) / kXcds * kXcds)), b);
-  }
+  for (int64_t b = 0; b < total && e == hipSuccess; b += kMaxTileBlocks)
+    e = f(dim3((uint32_t)std::min(total - b, kMaxTileBlocks)), b);
   return e;
 }
 
@@ -618,7 +738,7 @@ constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 template <bool GATED>
 using RowsTile = TileProduct<256, 256, 2, 4, false, false, GATED>;
-using RowsGradTile = TileProduct<256, 256, 2, 4, false, true, false>;
+using RowsGradTile = TileProduct<128, 256, 1, 4, false, true, false>;
 using WgradTile = TileProduct<256, 256, 2, 4, true, true, false>;
 
 }  // namespace
@@ -628,12 +748,11 @@ hipError_t launch_expert_rows(const ExpertDims& x, const int32_t* off, const uin
                               uint16_t* y, uint16_t* pre, hipStream_t s) {
   auto go = [&](auto tile) {
     using P = decltype(tile);
-    const int ntiles = ceil_div(x.N, P::GATED ? P::BN / 2 : P::BN);
-    const int64_t total = ((int64_t)x.rows / P::BM + x.E) * ntiles;
-    return in_ranges(total, [&](dim3 grid, int64_t b) {
-      return launch(MOE_KERNEL_EXPERT_ROWS, expert_rows_kernel<P>, grid, dim3(P::kThreads), 0, s, x,
+    const TileGrid<P::BM, P::BN> grid(1, x.rows / P::BM + x.E, ceil_div(x.N, P::GATED ? P::BN / 2 : P::BN));
+    return in_ranges(grid.blocks(), [&](dim3 blocks, int64_t b) {
+      return launch(MOE_KERNEL_EXPERT_ROWS, expert_rows_kernel<P>, blocks, dim3(P::kThreads), 0, s, x,
                     off, reinterpret_cast<const char*>(a), reinterpret_cast<const char*>(w), bias,
-                    residual, y, pre, b, total, ntiles);
+                    residual, y, pre, grid, b);
     });
   };
   if (gated(x.act)) return go(RowsTile<true>());
@@ -643,24 +762,22 @@ hipError_t launch_expert_rows(const ExpertDims& x, const int32_t* off, const uin
 hipError_t launch_expert_rows_grad(const ExpertDims& x, const int32_t* off, const uint16_t* gz,
                                    const uint16_t* w, uint16_t* gx, hipStream_t s) {
   using P = RowsGradTile;
-  const int ntiles = ceil_div(x.K, P::BN);
-  const int64_t total = ((int64_t)x.rows / P::BM + x.E) * ntiles;
-  return in_ranges(total, [&](dim3 grid, int64_t b) {
-    return launch(MOE_KERNEL_EXPERT_ROWS_GRAD, expert_rows_grad_kernel<P>, grid, dim3(P::kThreads), 0,
+  const TileGrid<P::BM, P::BN> grid(1, x.rows / P::BM + x.E, ceil_div(x.K, P::BN));
+  return in_ranges(grid.blocks(), [&](dim3 blocks, int64_t b) {
+    return launch(MOE_KERNEL_EXPERT_ROWS_GRAD, expert_rows_grad_kernel<P>, blocks, dim3(P::kThreads), 0,
                   s, x, off, reinterpret_cast<const char*>(gz), reinterpret_cast<const char*>(w), gx,
-                  b, total, ntiles);
+                  grid, b);
   });
 }
 
 hipError_t launch_expert_wgrad(const ExpertDims& x, const int32_t* off, const uint16_t* gz,
                                const uint16_t* a, void* gw, bool f32, hipStream_t s) {
   using P = WgradTile;
-  const int mtiles = ceil_div(x.Z, P::BM), ntiles = ceil_div(x.K, P::BN);
-  const int64_t total = (int64_t)x.E * mtiles * ntiles;
-  return in_ranges(total, [&](dim3 grid, int64_t b) {
+  const TileGrid<P::BM, P::BN> grid(x.E, ceil_div(x.Z, P::BM), ceil_div(x.K, P::BN));
+  return in_ranges(grid.blocks(), [&](dim3 blocks, int64_t b) {
     return launch(MOE_KERNEL_EXPERT_WGRAD, f32 ? expert_wgrad_kernel<P, true> : expert_wgrad_kernel<P, false>,
-                  grid, dim3(P::kThreads), 0, s, x, off, reinterpret_cast<const char*>(gz),
-                  reinterpret_cast<const char*>(a), gw, b, total, mtiles, ntiles);
+                  blocks, dim3(P::kThreads), 0, s, x, off, reinterpret_cast<const char*>(gz),
+                  reinterpret_cast<const char*>(a), gw, grid, b);
   });
 }
 
