@@ -30,7 +30,6 @@
 // contiguous contraction are sent past the descriptor's end, so that they
 // read as zeros on both sides.
 #include <algorithm>
-#include <type_traits>
 
 #include "layer_internal.h"
 
@@ -89,7 +88,26 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_buffer(const char* p, 
 
 // ---- activations
 
-__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(-0.70710678118654752f * z); }
+// The normal distribution Phi(z), and bell = exp(-z^2 / 2).  With x = |z| / sqrt 2,
+// erfc(x) = bell * t * P(t), t = 1 / (1 + 0.425 x): P is a polynomial of degree
+// 7, fitted (iteratively reweighted least squares at Chebyshev nodes) to a
+// relative error below 2e-7 over |z| < 15, so small tails keep their digits.
+// A seventh of the instructions of the math library's erfc, which dominated
+// the epilogue of small products.
+__device__ __forceinline__ float normal_cdf(float z, float& bell) {
+  bell = __expf(-0.5f * z * z);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.425f * 0.70710678118654752f, fabsf(z), 1.0f));
+  float p = 0.07013754546642303f;
+  p = __builtin_fmaf(p, t, -0.30760806798934937f);
+  p = __builtin_fmaf(p, t, 0.39813491702079773f);
+  p = __builtin_fmaf(p, t, -0.0946105495095253f);
+  p = __builtin_fmaf(p, t, 0.25057145953178406f);
+  p = __builtin_fmaf(p, t, 0.2020537555217743f);
+  p = __builtin_fmaf(p, t, 0.24162858724594116f);
+  p = __builtin_fmaf(p, t, 0.23969215154647827f);
+  const float tail = 0.5f * bell * t * p;
+  return z < 0.0f ? tail : 1.0f - tail;
+}
 
 __device__ __forceinline__ float logistic(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
@@ -110,7 +128,10 @@ __device__ __forceinline__ void act_values(int act, float (&z)[8]) {
     case MOE_ACT_GELU:
     case MOE_ACT_GEGLU:
 #pragma unroll
-      for (int q = 0; q < 8; ++q) z[q] *= normal_cdf(z[q]);
+      for (int q = 0; q < 8; ++q) {
+        float bell;
+        z[q] *= normal_cdf(z[q], bell);
+      }
       break;
     default: break;
   }
@@ -140,9 +161,10 @@ __device__ __forceinline__ void act_slopes(int act, const float (&z)[8], float (
     case MOE_ACT_GEGLU:
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const float p = normal_cdf(z[q]);
+        float bell;
+        const float p = normal_cdf(z[q], bell);
         value[q] = z[q] * p;
-        slope[q] = p + z[q] * 0.3989422804014327f * __expf(-0.5f * z[q] * z[q]);
+        slope[q] = p + z[q] * 0.3989422804014327f * bell;
       }
       break;
     default:
@@ -154,35 +176,91 @@ __device__ __forceinline__ void act_slopes(int act, const float (&z)[8], float (
   }
 }
 
-// ---- which expert and rows a slot of BM rows stands for
+// ---- which expert and rows a tile of rows stands for
 
-struct Segment {
-  int e;      // expert
-  int row;    // first row
-  int rows;   // rows of the tile (<= 0: the slot is not used)
-  int left;   // rows of the expert from `row` on
+// The experts' row tiles, numbered without gaps: expert e's are
+// [first[e], first[e + 1]).  Built in LDS by every block.
+struct RowTiles {
+  int32_t first[MOE_MAX_EXPERTS + 1];
+  int32_t wave[16];
+
+  // BM rows a tile; THREADS threads, all of the block.
+  template <int BM, int THREADS>
+  __device__ __forceinline__ void build(const int32_t* off, int E) {
+    constexpr int per = MOE_MAX_EXPERTS / THREADS;  // consecutive experts a thread
+    static_assert(per * THREADS == MOE_MAX_EXPERTS && THREADS / kWave <= 16);
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave;
+    int n[per], sum = 0;
+#pragma unroll
+    for (int q = 0; q < per; ++q) {
+      const int e = tid * per + q;
+      n[q] = e < E ? (off[e + 1] - off[e] + BM - 1) / BM : 0;
+      sum += n[q];
+    }
+    int before = sum;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const int o = __shfl_up(before, d);
+      if (lane >= d) before += o;
+    }
+    if (lane == kWave - 1) wave[wv] = before;
+    __syncthreads();
+    before -= sum;
+    for (int q = 0; q < wv; ++q) before += wave[q];
+#pragma unroll
+    for (int q = 0; q < per; ++q) {
+      const int e = tid * per + q;
+      if (e < E) first[e] = before;
+      before += n[q];
+      if (e == E - 1) first[E] = before;
+    }
+    __syncthreads();
+  }
 };
 
-// The last expert whose first slot, off[e] / BM + e, is <= slot.  Two rounds
-// of one load a lane: every ceil(E / 64)-th expert, then those in between.
-__device__ __forceinline__ Segment find_segment(const int32_t* off, int E, int slot, int bm) {
+struct Segment {
+  int e;     // expert
+  int row;   // first row
+  int rows;  // rows of the tile
+};
+
+// The expert of row tile m: the last one with first[e] <= m.  Two rounds of
+// one LDS read a lane: every ceil(E / 64)-th expert, then those in between.
+template <int BM>
+__device__ __forceinline__ Segment segment_of(const RowTiles& t, const int32_t* off, int E, int m) {
   const int lane = threadIdx.x & (kWave - 1);
   const int step = (E + kWave - 1) / kWave;
   const int e1 = lane * step;
-  const bool in1 = e1 < E && off[min(e1, E)] / bm + e1 <= slot;
-  int e = (__popcll(__ballot(in1)) - 1) * step;  // lane 0 is always in
+  int e = (__popcll(__ballot(e1 < E && t.first[min(e1, E)] <= m)) - 1) * step;  // lane 0 is in
   if (step > 1) {
     const int e2 = e + lane;
-    const bool in2 = lane < step && e2 < E && off[min(e2, E)] / bm + e2 <= slot;
-    e += __popcll(__ballot(in2)) - 1;
+    e += __popcll(__ballot(lane < step && e2 < E && t.first[min(e2, E)] <= m)) - 1;
+  }
+  Segment s;
+  s.e = __builtin_amdgcn_readfirstlane(e);
+  s.row = off[s.e] + (m - __builtin_amdgcn_readfirstlane(t.first[s.e])) * BM;
+  s.rows = min(BM, off[s.e + 1] - s.row);
+  return s;
+}
+
+// The same for slots of BM rows that need no table: expert e's slots start at
+// off[e] / BM + e, which leaves at least ceil(rows / BM) slots each and makes
+// rows / BM + E in all; slots that no row falls into have rows <= 0.
+__device__ __forceinline__ Segment segment_of_slot(const int32_t* off, int E, int slot, int bm) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int step = (E + kWave - 1) / kWave;
+  const int e1 = lane * step;
+  int e = (__popcll(__ballot(e1 < E && off[min(e1, E)] / bm + e1 <= slot)) - 1) * step;
+  if (step > 1) {
+    const int e2 = e + lane;
+    e += __popcll(__ballot(lane < step && e2 < E && off[min(e2, E)] / bm + e2 <= slot)) - 1;
   }
   e = __builtin_amdgcn_readfirstlane(e);
   Segment s;
   const int o0 = off[e], o1 = off[e + 1];
   s.e = e;
   s.row = o0 + (slot - (o0 / bm + e)) * bm;
-  s.left = o1 - s.row;
-  s.rows = min(s.left, bm);
+  s.rows = min(o1 - s.row, bm);
   return s;
 }
 
@@ -205,44 +283,38 @@ struct TileGrid {
   int grids, mtiles, ntiles;
   int mgroups, ngroups;
 
-  TileGrid(int grids_, int mtiles_, int ntiles_)
+  __host__ __device__ TileGrid(int grids_, int mtiles_, int ntiles_)
       : grids(grids_), mtiles(mtiles_), ntiles(ntiles_),
         mgroups((mtiles_ + kGroupM - 1) / kGroupM), ngroups((ntiles_ + kGroupN - 1) / kGroupN) {}
-  // Blocks of all launches together.
-  int64_t blocks() const {
-    const int64_t groups = (int64_t)grids * mgroups * ngroups;
-    return (groups + kXcds - 1) / kXcds * kXcds * kTiles;
+  // Numbers at() takes: those of tiles, and some that are not live.
+  __host__ __device__ int numbers() const {
+    return (grids * mgroups * ngroups + kXcds - 1) / kXcds * kXcds * kTiles;
   }
-  __device__ __forceinline__ Tile at(int64_t block) const {
-    const int64_t i = block / kXcds;
-    const int64_t group = i / kTiles * kXcds + block % kXcds;
-    const int in = (int)(i % kTiles);
+  __device__ __forceinline__ Tile at(int number) const {
+    const int i = number / kXcds;
+    const int group = i / kTiles * kXcds + number % kXcds;
+    const int in = i % kTiles;
     const int per = mgroups * ngroups;
+    const int g = group % per;
     Tile t;
-    t.grid = (int)(group / per);
-    const int g = (int)(group % per);
+    t.live = group / per < grids;
+    t.grid = group / per;
     t.m = g / ngroups * kGroupM + in / kGroupN;
     t.n = g % ngroups * kGroupN + in % kGroupN;
-    t.live = t.grid < grids && t.m < mtiles && t.n < ntiles;
+    t.live = t.live && t.m < mtiles && t.n < ntiles;
     return t;
   }
 };
 
 // ---- the tile product
 
-// One operand's tile: where its bytes are and how far they go.
-struct Operand {
-  const char* base;   // row 0, contraction 0
-  uint32_t ld;        // bytes between rows of memory
-  uint32_t bytes;     // contiguous contraction: bytes from base to the end of the tile's rows
-};
-
 template <int BM_, int BN_, int WM_, int WN_, bool AT_, bool BT_, bool GATED_>
 struct TileProduct {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
   static constexpr bool AT = AT_, BT = BT_, GATED = GATED_;
   static constexpr int kNW = WM * WN, kThreads = kNW * kWave;
-  static constexpr int TM = BM / WM, TN = BN / WN, MI = TM / 16, NJ = TN / 16;
+  // A wave computes every WM-th 16 rows (MI of them) and TN consecutive columns.
+  static constexpr int TN = BN / WN, MI = BM / WM / 16, NJ = TN / 16;
   static constexpr int kABytes = BM * kBK * 2, kBBytes = BN * kBK * 2;
   static constexpr int kStage = kABytes + kBBytes;
   static constexpr int kStages = 3;
@@ -288,155 +360,199 @@ struct TileProduct {
     bf16x8 a[MI], b[NJ];
   };
 
-  f32x4 acc[MI][NJ];
+  // A tile's operands, as far as they have been loaded.
+  struct Cursor {
+    const char *a, *b;         // row 0, contraction 0 of the tile
+    uint32_t a_bytes, b_bytes; // contiguous contraction: bytes to the end of the tile's rows;
+                               // transposed: bytes from a memory row's start to the tile's columns
+    int len;                   // contraction elements
+    int step;                  // step that is loaded next
+  };
+  // Steps of a tile: an even number, for the two sets of fragment registers,
+  // and at least four, so that the loads are never more than a tile ahead.
+  static __device__ __forceinline__ int steps_of(int len) {
+    return max((len + 2 * kBK - 1) / (2 * kBK), 2) * 2;
+  }
 
-  __device__ __forceinline__ void clear() {
+  f32x4 acc[MI][NJ];
+  uint32_t va[QA], vb[QB];  // byte offsets of this lane's loads from a step's base
+  uint32_t lda, ldb;        // bytes between memory rows
+  char* lds;
+  int wave, lane, m0, n0;
+  int put;                  // LDS offset of the stage to load next
+
+  // gate_up: memory rows from the gate's to the up projection's row (gated only).
+  __device__ __forceinline__ TileProduct(char* lds_, uint32_t lda_, uint32_t ldb_, int gate_up)
+      : lda(lda_), ldb(ldb_), lds(lds_), put(0) {
+    lane = threadIdx.x % kWave;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    m0 = wave / WN * 16;
+    n0 = wave % WN * TN;
+#pragma unroll
+    for (int q = 0; q < QA; ++q)
+      va[q] = AT ? offset_t<BM>(lda, wave, lane, q)
+                 : (uint32_t)row_of(q) * lda + chunk<false>() * 16;
+#pragma unroll
+    for (int q = 0; q < QB; ++q)
+      vb[q] = BT ? offset_t<BN>(ldb, wave, lane, q)
+                 : (uint32_t)b_row(row_of(q), gate_up) * ldb + chunk<true>() * 16;
+  }
+
+  // Contiguous contraction: the LDS row of this lane's q-th load, and the chunk
+  // of a step that it loads (the same for every q).
+  __device__ __forceinline__ int row_of(int q) const { return (q * kNW + wave) * 16 + lane / 4; }
+  template <bool B>
+  __device__ __forceinline__ int chunk() const {
+    static_assert(kNW % 2 == 0);
+    return (lane & 3) ^ swizzle<B>(row_of(0));
+  }
+
+  // Loads the cursor's step into the stage at `to`.
+  __device__ __forceinline__ void load(Cursor& c, char* to) {
+    const int done = c.step * kBK, left = c.len - done;
+    issue<AT, false, QA>(c.a, lda, c.a_bytes, va, done, left, to + wave * 1024);
+    issue<BT, true, QB>(c.b, ldb, c.b_bytes, vb, done, left, to + kABytes + wave * 1024);
+    ++c.step;
+  }
+
+  static __device__ __forceinline__ int stage_after(int at) {
+    return at == (kStages - 1) * kStage ? 0 : at + kStage;
+  }
+
+  // Loads the first tile's first three steps.
+  __device__ __forceinline__ void start(Cursor& c) {
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) load(c, lds + i * kStage);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+
+  // acc = A B of one tile of `steps` steps.  rows: result rows that are wanted
+  // (the others' products are skipped, a quarter of the tile at a time).
+  // next(cursor) sets the cursor to the following tile (or to an empty one).
+  //
+  // While the fragments of step s (in registers) are multiplied, those of
+  // step s + 1 are read from LDS and the loads of steps s + 2 and s + 3 are
+  // under way; steps past the end are the next tile's, so the loads never
+  // pause and run on under the epilogue.  One barrier a step: before it a
+  // wave waits for its own fragments of step s (so stage s is free after it,
+  // for step s + 3) and for its own loads of step s + 1 (so they can be read
+  // after it).  Loads come back in the order they were issued, so with at most
+  // one step's count of operations under way, those are the last step's.
+  template <typename Next>
+  __device__ __forceinline__ void run(Cursor& c, const Next& next, int steps, int rows) {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-
-  // acc += A B over `len` contraction elements.  rows: result rows that are
-  // wanted (the others' products are skipped, 16 rows at a time).  gate_up:
-  // memory rows from the gate's to the up projection's row (gated only).
-  //
-  // While the fragments of step s (in registers) are multiplied, those of
-  // step s + 1 are read from LDS and the loads of steps s + 2 and s + 3 are
-  // under way.  One barrier a step: before it a wave waits for its own
-  // fragments of step s (so stage s is free after it, for step s + 3) and for
-  // its own loads of step s + 1 (so they can be read after it).  Steps past
-  // the end load zeros through empty descriptors, which keeps the number of
-  // loads under way the same in every step.
-  __device__ __forceinline__ void run(const Operand& a, const Operand& b, int len, int rows,
-                                      int gate_up, char* lds) {
-    const int m0 = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) / WN * TM;
-    const int used = min(max((rows - m0 + 15) / 16, 0), MI);
-    if (used == MI)
-      sweep<true>(a, b, len, MI, gate_up, lds);
-    else
-      sweep<false>(a, b, len, used, gate_up, lds);
-  }
-
-  template <bool FULL>
-  __device__ __forceinline__ void sweep(const Operand& a, const Operand& b, int len, int used,
-                                        int gate_up, char* lds) {
-    const int tid = threadIdx.x, lane = tid % kWave;
-    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    uint32_t va[QA], vb[QB];
-    int ca[QA], cb[QB];  // chunk of the step a lane loads (contiguous contraction)
-#pragma unroll
-    for (int q = 0; q < QA; ++q) {
-      const int r = (q * kNW + wave) * 16 + lane / 4;
-      ca[q] = AT ? 0 : (lane & 3) ^ swizzle<false>(r);
-      va[q] = AT ? offset_t<BM>(a.ld, wave, lane, q) : (uint32_t)r * a.ld + ca[q] * 16;
-    }
-#pragma unroll
-    for (int q = 0; q < QB; ++q) {
-      const int r = (q * kNW + wave) * 16 + lane / 4;
-      cb[q] = BT ? 0 : (lane & 3) ^ swizzle<true>(r);
-      vb[q] = BT ? offset_t<BN>(b.ld, wave, lane, q)
-                 : (uint32_t)b_row(r, gate_up) * b.ld + cb[q] * 16;
-    }
-    const int m0 = wave / WN * TM, n0 = wave % WN * TN;
-    const int steps = (len + kBK - 1) / kBK;
-    auto load = [&](int step, char* to) {
-      const int done = step * kBK, left = len - done;
-      issue<AT, QA>(a, va, ca, done, left, to + wave * 1024);
-      issue<BT, QB>(b, vb, cb, done, left, to + kABytes + wave * 1024);
-    };
-    auto read = [&](Fragments& f, const char* from) {
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) f.b[j] = fragment<BT, true, BN>(from + kABytes, n0, j, lane);
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-        if (FULL || i < used) f.a[i] = fragment<AT, false, BM>(from, m0, i, lane);
-    };
-    int put = 0, get = kStage;  // LDS offsets of the next stage to load and to read
-    auto step = [&](int s, const Fragments& now, Fragments& next) {
-      wait_and_meet<QA + QB>();
-      refill(load, read, s + 3, next, lds + put, lds + get);
-      put = put == (kStages - 1) * kStage ? 0 : put + kStage;
-      get = get == (kStages - 1) * kStage ? 0 : get + kStage;
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-        if (FULL || i < used)
-#pragma unroll
-          for (int j = 0; j < NJ; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now.b[j], now.a[i], acc[i][j], 0, 0, 0);
-      if constexpr (FULL) interleave();
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    load(0, lds);
-    load(1, lds + kStage);
-    load(2, lds + 2 * kStage);
-    wait_and_meet<2 * (QA + QB)>();
-    Fragments f0{}, f1{};
-    read(f0, lds);
+    Fragments f0, f1;
+    wait_and_meet<-1>();  // the tile's first three steps have landed, for every wave
+    read(f0, lds + put);
     for (int s = 0; s < steps; s += 2) {
-      step(s, f0, f1);
-      if (s + 1 < steps) step(s + 1, f1, f0);
+      step(c, s == 0, rows, f0, f1);
+      // Tiles have an even number of steps and the cursor is three or four
+      // ahead here, so it comes to a tile's end in this place.
+      if (c.step == steps) next(c);
+      step(c, s == 0, rows, f1, f0);
     }
-    wait_and_meet<0>();  // nothing may land in LDS after the block has ended
+    // What is under way has landed before the epilogue's stores are issued, so
+    // the next tile's first steps need not wait for those.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+
+  // One step.  landed: what it reads has landed.  (The last step of a tile
+  // reads the next tile's first fragments, which that tile reads again.)
+  __device__ __forceinline__ void step(Cursor& c, bool landed, int rows, const Fragments& now,
+                                       Fragments& then) {
+    if (landed)
+      wait_and_meet<-1>();
+    else
+      wait_and_meet<QA + QB>();
+    refill(c, then, lds + put, lds + stage_after(put));
+    put = stage_after(put);
+    multiply<0>(now);
+    interleave();
+    __builtin_amdgcn_sched_barrier(0);
+    if (rows > kQuarter) multiply<1>(now);
+    __builtin_amdgcn_sched_barrier(0);
+    if (rows > 2 * kQuarter) multiply<2>(now);
+    __builtin_amdgcn_sched_barrier(0);
+    if (rows > 3 * kQuarter) multiply<3>(now);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // Quarter Q of the tile's rows.
+  static constexpr int kQuarter = BM / 4;
+  template <int Q>
+  __device__ __forceinline__ void multiply(const Fragments& f) {
+#pragma unroll
+    for (int i = Q * MI / 4; i < (Q + 1) * MI / 4; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
+  }
+
+  // Asks the scheduler to start with products (whose fragments have been
+  // waited for) and to spread the loads and the reads between them.
+  static __device__ __forceinline__ void interleave() {
+    constexpr int loads = QA + QB, reads = MI * (AT ? 2 : 1) + NJ * (BT ? 2 : 1);
+    constexpr int products = MI * NJ / 4;
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix instructions
+#pragma unroll
+    for (int i = 1; i < products; ++i) {
+      constexpr int each = (reads + products - 2) / (products - 1);
+      __builtin_amdgcn_sched_group_barrier(0x100, each, 0);  // LDS reads
+      if (i <= loads) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);  // load
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    }
+  }
+
+  __device__ __forceinline__ void read(Fragments& f, const char* from) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) f.b[j] = fragment<BT, true, BN>(from + kABytes, n0, j, lane);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) f.a[i] = fragment<AT, false, BM>(from, m0, i * WM, lane);
   }
 
   // The loads of a later step and the reads of the next.  The two stages are
   // different ones, and saying so (restrict) matters: where the compiler sees
   // that a read from LDS may touch what a load to LDS writes, it waits for
   // every load under way before the read.
-  template <typename L, typename R>
-  static __device__ __forceinline__ void refill(const L& load, const R& read, int step,
-                                                Fragments& next, char* __restrict__ to,
-                                                const char* __restrict__ from) {
-    load(step, to);
-    read(next, from);
+  __device__ __forceinline__ void refill(Cursor& c, Fragments& f, char* __restrict__ to,
+                                         const char* __restrict__ from) {
+    load(c, to);
+    read(f, from);
   }
 
-  // Waits until at most N of this wave's loads to LDS and none of its LDS
-  // reads are under way, then for the block's other waves.
+  // Waits until none of this wave's LDS reads and at most N (< 0: any number)
+  // of its loads are under way, then for the block's other waves.
   template <int N>
   static __device__ __forceinline__ void wait_and_meet() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+    if constexpr (N < 0)
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
     __builtin_amdgcn_sched_barrier(0);
   }
 
-  // Asks the scheduler to start with products (whose fragments have been
-  // waited for) and to spread the loads and the reads over the rest.
-  static __device__ __forceinline__ void interleave() {
-    constexpr int loads = QA + QB, reads = MI * (AT ? 2 : 1) + NJ * (BT ? 2 : 1);
-    constexpr int products = MI * NJ, each = (products - 2) / reads;
-    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);  // matrix instructions
-#pragma unroll
-    for (int i = 0; i < reads; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
-      if (i < loads) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);  // load
-      __builtin_amdgcn_sched_group_barrier(0x008, each, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(0x008, products - 2 - reads * each, 0);
-  }
-
-  template <bool T, int Q>
-  static __device__ __forceinline__ void issue(const Operand& o, const uint32_t (&v)[Q],
-                                               const int (&c)[Q], int done, int left, char* at) {
+  template <bool T, bool B, int Q>
+  __device__ __forceinline__ void issue(const char* from, uint32_t ld, uint32_t limit,
+                                        const uint32_t (&v)[Q], int done, int left, char* at) const {
     const char* base;
     uint32_t bytes;
     if constexpr (T) {
-      base = o.base + (int64_t)done * o.ld;
-      bytes = (uint32_t)max(min(left, kBK), 0) * o.ld;
-      bytes = bytes > o.bytes ? bytes - o.bytes : 0;  // o.bytes: the tile's first column
+      base = from + (int64_t)done * ld;
+      bytes = (uint32_t)max(min(left, kBK), 0) * ld;
+      bytes = bytes > limit ? bytes - limit : 0;
     } else {
-      base = o.base + (int64_t)done * 2;
-      bytes = left > 0 && o.bytes > (uint32_t)done * 2 ? o.bytes - done * 2 : 0;
+      base = from + (int64_t)done * 2;
+      bytes = left > 0 && limit > (uint32_t)done * 2 ? limit - done * 2 : 0;
     }
     const __amdgpu_buffer_rsrc_t r = uniform_buffer(base, bytes);
+    const bool in = T || chunk<B>() * 8 < left;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      uint32_t off = v[q];
-      if constexpr (!T)
-        if (left < kBK) off = c[q] * 8 < left ? off : kPast;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void*)(at + q * kNW * 1024), 16, off, 0, 0,
-                                               0);
-    }
+    for (int q = 0; q < Q; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void*)(at + q * kNW * 1024), 16,
+                                               in ? v[q] : kPast, 0, 0, 0);
   }
 
   template <bool T, bool B, int W>
@@ -462,102 +578,146 @@ struct TileProduct {
 // columns are consecutive: lane / 16 * 16 + j * 4 + 0..3 of the wave's 64
 // (gated: lane / 16 * 8 + (j & 1) * 4 of its 32, j >> 1 the gate or up).
 
+// Blocks of a launch: each CU gets as many as fit its LDS, and every block
+// computes one tile after another (numbers blockIdx.x, + gridDim.x, ...).
+constexpr int kCus = 256;
+template <typename P>
+constexpr int blocks_at_once() {
+  return kCus * (P::kLds + (int)sizeof(RowTiles) <= 80 * 1024 ? 2 : 1);
+}
+
 // ---- rows: y = act(x w^T + bias) + residual
+
+// The epilogue of four of a lane's rows (of the wave's 16 * MI), columns c0 on:
+// i0.. are the accumulator's rows.
+template <typename P, int I0>
+__device__ __forceinline__ void rows_epilogue(const P& p, const ExpertDims& x, const Segment& s,
+                                              int c0, const float (&bz)[16],
+                                              const uint16_t* residual, uint16_t* y,
+                                              uint16_t* pre) {
+  constexpr int kRows = 4, kHalves = P::GATED ? 1 : 2;  // rows, and 8-column pieces of y in a row
+  int64_t row[kRows];
+  bool ok[kRows];
+  u32x4 res[kRows][kHalves];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int m = p.m0 + (I0 + i) * (P::WM * 16) + (p.lane & 15);
+    ok[i] = m < s.rows;
+    row[i] = s.row + (ok[i] ? m : 0);
+  }
+  if (residual != nullptr) {  // all loads before the first use
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+        res[i][h] = *reinterpret_cast<const u32x4*>(residual + row[i] * x.N +
+                                                    (c0 + h * 8 < x.N ? c0 + h * 8 : 0));
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    float z[2][8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = j * 4 + q;
+        z[n / 8][n % 8] = p.acc[I0 + i][j][q] + bz[n];
+      }
+    if (!ok[i]) continue;
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+      const int col = c0 + h * 8;
+      if (col >= x.N) continue;
+      float out[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) out[q] = z[h][q];
+      if (pre != nullptr) {
+        *reinterpret_cast<u32x4*>(pre + row[i] * x.Z + col) = pack8(z[h]);
+        if constexpr (P::GATED)
+          *reinterpret_cast<u32x4*>(pre + row[i] * x.Z + x.N + col) = pack8(z[1]);
+      }
+      act_values(x.act, out);
+      if constexpr (P::GATED) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) out[q] *= z[1][q];
+      }
+      if (residual != nullptr) {
+        float r[8];
+        unpack8(res[i][h], r);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) out[q] += r[q];
+      }
+      *reinterpret_cast<u32x4*>(y + row[i] * x.N + col) = pack8(out);
+    }
+  }
+}
 
 template <typename P>
 __global__ __launch_bounds__(P::kThreads, 2) void expert_rows_kernel(
     ExpertDims x, const int32_t* __restrict__ off, const char* __restrict__ a,
     const char* __restrict__ w, const float* __restrict__ bias,
     const uint16_t* __restrict__ residual, uint16_t* __restrict__ y, uint16_t* __restrict__ pre,
-    TileGrid<P::BM, P::BN> grid, int64_t base) {
-  __shared__ __align__(1024) char lds[P::kLds];
+    int ntiles) {
+  __shared__ __align__(1024) char lds[P::kLds + sizeof(RowTiles)];
+  RowTiles& table = *reinterpret_cast<RowTiles*>(lds + P::kLds);
   constexpr int kCols = P::GATED ? P::BN / 2 : P::BN;  // columns of y a tile
-  const Tile tile = grid.at(base + blockIdx.x);
-  if (!tile.live) return;
-  const Segment s = find_segment(off, x.E, tile.m, P::BM);
-  if (s.rows <= 0) return;
-  const int n0 = tile.n * kCols;
+  table.build<P::BM, P::kThreads>(off, x.E);
+  const TileGrid<P::BM, P::BN> grid(1, __builtin_amdgcn_readfirstlane(table.first[x.E]), ntiles);
+  const int numbers = grid.numbers();
   const uint32_t ld = (uint32_t)x.K * 2;
-  Operand oa{a + (int64_t)s.row * ld, ld, (uint32_t)s.rows * ld};
-  Operand ob{w + ((int64_t)s.e * x.Z + n0) * ld, ld, (uint32_t)(x.Z - n0) * ld};
-  P p;
-  p.clear();
-  p.run(oa, ob, x.K, s.rows, x.N, lds);
-
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int g = lane >> 4;
-  const int m0 = wave / P::WN * P::TM + (lane & 15);
-  const int c0 = n0 + wave % P::WN * (P::GATED ? 32 : 64) + g * (P::GATED ? 8 : 16);
-  float bz[16];
-#pragma unroll
-  for (int q = 0; q < 16; ++q) bz[q] = 0.0f;
-  if (bias != nullptr) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int col = P::GATED ? c0 : c0 + h * 8;
-      if (col < x.N) {
-        const f32x4* q = reinterpret_cast<const f32x4*>(bias + (int64_t)s.e * x.Z + col +
-                                                        (P::GATED ? h * x.N : 0));
-        const f32x4 lo = q[0], hi = q[1];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          bz[h * 8 + i] = lo[i];
-          bz[h * 8 + 4 + i] = hi[i];
-        }
-      }
+  // The tile that is loaded, at most one ahead of the one that is multiplied.
+  int number = blockIdx.x, n_ahead = 0;
+  Segment ahead{0, 0, 0};
+  auto next = [&](typename P::Cursor& c) {
+    c = {a, w, 0, 0, 0, 0};  // no tile left: loads nothing
+    ahead.rows = 0;
+    for (; number < numbers; number += gridDim.x) {
+      const Tile t = grid.at(number);
+      if (!t.live) continue;
+      const Segment s = ahead = segment_of<P::BM>(table, off, x.E, t.m);
+      const int n0 = n_ahead = t.n * kCols;
+      c.a = a + (int64_t)s.row * ld;
+      c.a_bytes = (uint32_t)s.rows * ld;
+      c.b = w + ((int64_t)s.e * x.Z + n0) * ld;
+      c.b_bytes = (uint32_t)(x.Z - n0) * ld;
+      c.len = x.K;
+      number += gridDim.x;
+      break;
     }
-  }
+  };
+  typename P::Cursor c;
+  next(c);
+  P p(lds, ld, ld, x.N);
+  p.start(c);
+  while (ahead.rows > 0) {
+    const Segment s = ahead;
+    const int col0 = n_ahead;
+    p.run(c, next, P::steps_of(x.K), s.rows);
+
+    const int g = p.lane >> 4;
+    const int c0 = col0 + p.wave % P::WN * (P::GATED ? 32 : 64) + g * (P::GATED ? 8 : 16);
+    float bz[16];
 #pragma unroll
-  for (int i = 0; i < P::MI; ++i) {
-    const int m = m0 + i * 16;
-    if (m >= s.rows) continue;
-    const int64_t row = s.row + m;
-    float z[16];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) z[j * 4 + q] = p.acc[i][j][q] + bz[j * 4 + q];
-    if constexpr (P::GATED) {
-      if (c0 >= x.N) continue;
-      float gate[8], up[8], out[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        out[q] = gate[q] = z[q];
-        up[q] = z[8 + q];
-      }
-      act_values(x.act, out);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) out[q] *= up[q];
-      if (pre != nullptr) {
-        *reinterpret_cast<u32x4*>(pre + row * x.Z + c0) = pack8(gate);
-        *reinterpret_cast<u32x4*>(pre + row * x.Z + x.N + c0) = pack8(up);
-      }
-      if (residual != nullptr) {
-        float r[8];
-        unpack8(*reinterpret_cast<const u32x4*>(residual + row * x.N + c0), r);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) out[q] += r[q];
-      }
-      *reinterpret_cast<u32x4*>(y + row * x.N + c0) = pack8(out);
-    } else {
+    for (int q = 0; q < 16; ++q) bz[q] = 0.0f;
+    if (bias != nullptr) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int col = c0 + h * 8;
-        if (col >= x.N) continue;
-        float out[8];
+        const int col = P::GATED ? c0 : c0 + h * 8;
+        if (col < x.N) {
+          const f32x4* q = reinterpret_cast<const f32x4*>(bias + (int64_t)s.e * x.Z + col +
+                                                          (P::GATED ? h * x.N : 0));
+          const f32x4 lo = q[0], hi = q[1];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) out[q] = z[h * 8 + q];
-        if (pre != nullptr) *reinterpret_cast<u32x4*>(pre + row * x.Z + col) = pack8(out);
-        act_values(x.act, out);
-        if (residual != nullptr) {
-          float r[8];
-          unpack8(*reinterpret_cast<const u32x4*>(residual + row * x.N + col), r);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) out[q] += r[q];
+          for (int i = 0; i < 4; ++i) {
+            bz[h * 8 + i] = lo[i];
+            bz[h * 8 + 4 + i] = hi[i];
+          }
         }
-        *reinterpret_cast<u32x4*>(y + row * x.N + col) = pack8(out);
       }
     }
+    static_assert(P::MI % 4 == 0 && P::MI <= 8);
+    rows_epilogue<P, 0>(p, x, s, c0, bz, residual, y, pre);
+    if constexpr (P::MI > 4) rows_epilogue<P, 4>(p, x, s, c0, bz, residual, y, pre);
   }
 }
 
@@ -566,34 +726,54 @@ __global__ __launch_bounds__(P::kThreads, 2) void expert_rows_kernel(
 template <typename P>
 __global__ __launch_bounds__(P::kThreads, 2) void expert_rows_grad_kernel(
     ExpertDims x, const int32_t* __restrict__ off, const char* __restrict__ gz,
-    const char* __restrict__ w, uint16_t* __restrict__ gx, TileGrid<P::BM, P::BN> grid, int64_t base) {
-  __shared__ __align__(1024) char lds[P::kLds];
-  const Tile tile = grid.at(base + blockIdx.x);
-  if (!tile.live) return;
-  const Segment s = find_segment(off, x.E, tile.m, P::BM);
-  if (s.rows <= 0) return;
-  const int n0 = tile.n * P::BN;
+    const char* __restrict__ w, uint16_t* __restrict__ gx, int ntiles) {
+  __shared__ __align__(1024) char lds[P::kLds + sizeof(RowTiles)];
+  RowTiles& table = *reinterpret_cast<RowTiles*>(lds + P::kLds);
+  table.build<P::BM, P::kThreads>(off, x.E);
+  const TileGrid<P::BM, P::BN> grid(1, __builtin_amdgcn_readfirstlane(table.first[x.E]), ntiles);
+  const int numbers = grid.numbers();
   const uint32_t lda = (uint32_t)x.Z * 2, ldb = (uint32_t)x.K * 2;
-  Operand oa{gz + (int64_t)s.row * lda, lda, (uint32_t)s.rows * lda};
-  Operand ob{w + (int64_t)s.e * x.Z * ldb + n0 * 2, ldb, (uint32_t)n0 * 2};
-  P p;
-  p.clear();
-  p.run(oa, ob, x.Z, s.rows, 0, lds);
+  int number = blockIdx.x, n_ahead = 0;
+  Segment ahead{0, 0, 0};
+  auto next = [&](typename P::Cursor& c) {
+    c = {gz, w, 0, 0, 0, 0};
+    ahead.rows = 0;
+    for (; number < numbers; number += gridDim.x) {
+      const Tile t = grid.at(number);
+      if (!t.live) continue;
+      const Segment s = ahead = segment_of<P::BM>(table, off, x.E, t.m);
+      n_ahead = t.n * P::BN;
+      c.a = gz + (int64_t)s.row * lda;
+      c.a_bytes = (uint32_t)s.rows * lda;
+      c.b = w + (int64_t)s.e * x.Z * ldb + t.n * P::BN * 2;
+      c.b_bytes = (uint32_t)(t.n * P::BN * 2);
+      c.len = x.Z;
+      number += gridDim.x;
+      break;
+    }
+  };
+  typename P::Cursor c;
+  next(c);
+  P p(lds, lda, ldb, 0);
+  p.start(c);
+  while (ahead.rows > 0) {
+    const Segment s = ahead;
+    const int col0 = n_ahead;
+    p.run(c, next, P::steps_of(x.Z), s.rows);
 
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int m0 = wave / P::WN * P::TM + (lane & 15);
-  const int c0 = n0 + wave % P::WN * P::TN + (lane >> 4) * 4;
+    const int c0 = col0 + p.n0 + (p.lane >> 4) * 4;
 #pragma unroll
-  for (int i = 0; i < P::MI; ++i) {
-    const int m = m0 + i * 16;
-    if (m >= s.rows) continue;
+    for (int i = 0; i < P::MI; ++i) {
+      const int m = p.m0 + i * (P::WM * 16) + (p.lane & 15);
+      if (m >= s.rows) continue;
 #pragma unroll
-    for (int j = 0; j < P::NJ; ++j) {
-      const int col = c0 + j * 16;
-      if (col >= x.K) continue;
-      const f32x4 v = p.acc[i][j];
-      *reinterpret_cast<u32x2*>(gx + (int64_t)(s.row + m) * x.K + col) =
-          u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+      for (int j = 0; j < P::NJ; ++j) {
+        const int col = c0 + j * 16;
+        if (col >= x.K) continue;
+        const f32x4 v = p.acc[i][j];
+        *reinterpret_cast<u32x2*>(gx + (int64_t)(s.row + m) * x.K + col) =
+            u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+      }
     }
   }
 }
@@ -603,37 +783,55 @@ __global__ __launch_bounds__(P::kThreads, 2) void expert_rows_grad_kernel(
 template <typename P, bool F32>
 __global__ __launch_bounds__(P::kThreads, 2) void expert_wgrad_kernel(
     ExpertDims x, const int32_t* __restrict__ off, const char* __restrict__ gz,
-    const char* __restrict__ a, void* __restrict__ gw, TileGrid<P::BM, P::BN> grid, int64_t base) {
+    const char* __restrict__ a, void* __restrict__ gw, TileGrid<P::BM, P::BN> grid) {
   __shared__ __align__(1024) char lds[P::kLds];
-  const Tile tile = grid.at(base + blockIdx.x);
-  if (!tile.live) return;
-  const int e = tile.grid, z0 = tile.m * P::BM, n0 = tile.n * P::BN;
-  const int o0 = x.rows > 0 ? off[e] : 0, rows = x.rows > 0 ? off[e + 1] - o0 : 0;
+  const int numbers = grid.numbers();
   const uint32_t lda = (uint32_t)x.Z * 2, ldb = (uint32_t)x.K * 2;
-  Operand oa{gz + (int64_t)o0 * lda + z0 * 2, lda, (uint32_t)z0 * 2};
-  Operand ob{a + (int64_t)o0 * ldb + n0 * 2, ldb, (uint32_t)n0 * 2};
-  P p;
-  p.clear();
-  p.run(oa, ob, rows, x.Z - z0, 0, lds);
+  int number = blockIdx.x;
+  Tile ahead{0, 0, 0, false};
+  auto next = [&](typename P::Cursor& c) {
+    c = {gz, a, 0, 0, 0, 0};
+    ahead.live = false;
+    for (; number < numbers; number += gridDim.x) {
+      const Tile t = grid.at(number);
+      if (!t.live) continue;
+      ahead = t;
+      const int64_t o0 = x.rows > 0 ? off[t.grid] : 0;
+      c.a = gz + o0 * lda + t.m * P::BM * 2;
+      c.a_bytes = (uint32_t)(t.m * P::BM * 2);
+      c.b = a + o0 * ldb + t.n * P::BN * 2;
+      c.b_bytes = (uint32_t)(t.n * P::BN * 2);
+      c.len = x.rows > 0 ? off[t.grid + 1] - (int)o0 : 0;
+      number += gridDim.x;
+      break;
+    }
+  };
+  typename P::Cursor c;
+  next(c);
+  P p(lds, lda, ldb, 0);
+  p.start(c);
+  while (ahead.live) {
+    const Tile t = ahead;
+    p.run(c, next, P::steps_of(c.len), x.Z - t.m * P::BM);
 
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int m0 = z0 + wave / P::WN * P::TM + (lane & 15);
-  const int c0 = n0 + wave % P::WN * P::TN + (lane >> 4) * 4;
+    const int r0 = t.m * P::BM + p.m0 + (p.lane & 15);
+    const int c0 = t.n * P::BN + p.n0 + (p.lane >> 4) * 4;
 #pragma unroll
-  for (int i = 0; i < P::MI; ++i) {
-    const int m = m0 + i * 16;
-    if (m >= x.Z) continue;
+    for (int i = 0; i < P::MI; ++i) {
+      const int m = r0 + i * (P::WM * 16);
+      if (m >= x.Z) continue;
 #pragma unroll
-    for (int j = 0; j < P::NJ; ++j) {
-      const int col = c0 + j * 16;
-      if (col >= x.K) continue;
-      const f32x4 v = p.acc[i][j];
-      const int64_t at = ((int64_t)e * x.Z + m) * x.K + col;
-      if constexpr (F32)
-        *reinterpret_cast<f32x4*>(static_cast<float*>(gw) + at) = v;
-      else
-        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(gw) + at) =
-            u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+      for (int j = 0; j < P::NJ; ++j) {
+        const int col = c0 + j * 16;
+        if (col >= x.K) continue;
+        const f32x4 v = p.acc[i][j];
+        const int64_t at = ((int64_t)t.grid * x.Z + m) * x.K + col;
+        if constexpr (F32)
+          *reinterpret_cast<f32x4*>(static_cast<float*>(gw) + at) = v;
+        else
+          *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(gw) + at) =
+              u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+      }
     }
   }
 }
@@ -654,7 +852,7 @@ __global__ __launch_bounds__(kActCols * kActRows) void expert_act_grad_kernel(
   const int64_t tile = base + blockIdx.x;
   if (tile >= total) return;
   const int slot = (int)(tile / strips);
-  const Segment s = find_segment(off, x.E, slot, kBiasRows);
+  const Segment s = segment_of_slot(off, x.E, slot, kBiasRows);
   if (s.rows <= 0) return;
   const int c = threadIdx.x % kActCols, r0 = threadIdx.x / kActCols;
   const int col0 = (int)(tile % strips) * (kActCols * 8);
@@ -665,42 +863,57 @@ __global__ __launch_bounds__(kActCols * kActRows) void expert_act_grad_kernel(
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int q = 0; q < 8; ++q) sum[h][q] = 0.0f;
+  const bool act = x.act != MOE_ACT_NONE;
   if (col < x.N) {
-    for (int r = r0; r < s.rows; r += kActRows) {
-      const int64_t row = s.row + r;
-      float g[8], z[8], o[8];
-      unpack8(*reinterpret_cast<const u32x4*>(gy + row * x.N + col), g);
-      if (x.act == MOE_ACT_NONE) {
+    constexpr int kAhead = 4;  // rows whose loads are issued together
+    for (int r = r0; r < s.rows; r += kAhead * kActRows) {
+      u32x4 vg[kAhead], vz[kAhead], vu[kAhead];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) o[q] = g[q];
-      } else {
-        unpack8(*reinterpret_cast<const u32x4*>(pre + row * x.Z + col), z);
-        float value[8], slope[8];
-        act_slopes(x.act, z, value, slope);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) o[q] = g[q] * slope[q];
-        if (two) {
-          float up[8], u[8];
-          unpack8(*reinterpret_cast<const u32x4*>(pre + row * x.Z + x.N + col), up);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            o[q] *= up[q];
-            u[q] = g[q] * value[q];
-            sum[1][q] += u[q];
-          }
-          if (gz != nullptr) *reinterpret_cast<u32x4*>(gz + row * x.Z + x.N + col) = pack8(u);
-        }
-        if (gz != nullptr) *reinterpret_cast<u32x4*>(gz + row * x.Z + col) = pack8(o);
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t row = s.row + min(r + i * kActRows, s.rows - 1);
+        vg[i] = *reinterpret_cast<const u32x4*>(gy + row * x.N + col);
+        if (act) vz[i] = *reinterpret_cast<const u32x4*>(pre + row * x.Z + col);
+        if (two) vu[i] = *reinterpret_cast<const u32x4*>(pre + row * x.Z + x.N + col);
       }
 #pragma unroll
-      for (int q = 0; q < 8; ++q) sum[0][q] += o[q];
+      for (int i = 0; i < kAhead; ++i) {
+        if (r + i * kActRows >= s.rows) break;
+        const int64_t row = s.row + r + i * kActRows;
+        float g[8], o[8];
+        unpack8(vg[i], g);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) o[q] = g[q];
+        if (act) {
+          float z[8], value[8], slope[8];
+          unpack8(vz[i], z);
+          act_slopes(x.act, z, value, slope);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) o[q] *= slope[q];
+          if (two) {
+            float up[8], u[8];
+            unpack8(vu[i], up);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              o[q] *= up[q];
+              u[q] = g[q] * value[q];
+              sum[1][q] += u[q];
+            }
+            if (gz != nullptr) *reinterpret_cast<u32x4*>(gz + row * x.Z + x.N + col) = pack8(u);
+          }
+          if (gz != nullptr) *reinterpret_cast<u32x4*>(gz + row * x.Z + col) = pack8(o);
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum[0][q] += o[q];
+      }
     }
   }
   if (partial == nullptr) return;
-  for (int h = 0; h < (two ? 2 : 1); ++h) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (h == 1 && !two) break;
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 8; ++q) s_sum[r0][c * 8 + q] = h ? sum[1][q] : sum[0][q];
+    for (int q = 0; q < 8; ++q) s_sum[r0][c * 8 + q] = sum[h][q];
     __syncthreads();
     const int n = threadIdx.x;  // one column a thread
     float t = 0.0f;
@@ -719,8 +932,17 @@ __global__ __launch_bounds__(256) void expert_bias_sum_kernel(ExpertDims x,
   const int o0 = x.rows > 0 ? off[e] : 0, rows = x.rows > 0 ? off[e + 1] - o0 : 0;
   const int64_t first = o0 / kBiasRows + e;
   const int used = (rows + kBiasRows - 1) / kBiasRows;
+  const float* p = partial + first * x.Z + n;
   float t = 0.0f;
-  for (int i = 0; i < used; ++i) t += partial[(first + i) * x.Z + n];
+  int i = 0;
+  for (; i + 8 <= used; i += 8, p += (int64_t)8 * x.Z) {  // eight loads at a time, added in order
+    float v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = p[(int64_t)q * x.Z];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) t += v[q];
+  }
+  for (; i < used; ++i, p += x.Z) t += *p;
   gb[(int64_t)e * x.Z + n] = t;
 }
 
@@ -736,10 +958,23 @@ hipError_t in_ranges(int64_t total, F f) {
 
 constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+// Blocks for the row products: the most row tiles there can be are
+// rows / BM + E (the counts are only known on the device).
+template <typename P>
+dim3 row_blocks(const ExpertDims& x, int ntiles) {
+  const TileGrid<P::BM, P::BN> most(1, x.rows / P::BM + x.E, ntiles);
+  return dim3(std::min(most.numbers(), blocks_at_once<P>()));
+}
+
+template <typename T>
+struct Type {
+  using type = T;
+};
+
 template <bool GATED>
 using RowsTile = TileProduct<256, 256, 2, 4, false, false, GATED>;
 using RowsGradTile = TileProduct<128, 256, 1, 4, false, true, false>;
-using WgradTile = TileProduct<256, 256, 2, 4, true, true, false>;
+using WgradTile = TileProduct<128, 256, 1, 4, true, true, false>;
 
 }  // namespace
 
@@ -747,38 +982,33 @@ hipError_t launch_expert_rows(const ExpertDims& x, const int32_t* off, const uin
                               const uint16_t* w, const float* bias, const uint16_t* residual,
                               uint16_t* y, uint16_t* pre, hipStream_t s) {
   auto go = [&](auto tile) {
-    using P = decltype(tile);
-    const TileGrid<P::BM, P::BN> grid(1, x.rows / P::BM + x.E, ceil_div(x.N, P::GATED ? P::BN / 2 : P::BN));
-    return in_ranges(grid.blocks(), [&](dim3 blocks, int64_t b) {
-      return launch(MOE_KERNEL_EXPERT_ROWS, expert_rows_kernel<P>, blocks, dim3(P::kThreads), 0, s, x,
-                    off, reinterpret_cast<const char*>(a), reinterpret_cast<const char*>(w), bias,
-                    residual, y, pre, grid, b);
-    });
+    using P = typename decltype(tile)::type;
+    const int ntiles = ceil_div(x.N, P::GATED ? P::BN / 2 : P::BN);
+    return launch(MOE_KERNEL_EXPERT_ROWS, expert_rows_kernel<P>, row_blocks<P>(x, ntiles),
+                  dim3(P::kThreads), 0, s, x, off, reinterpret_cast<const char*>(a),
+                  reinterpret_cast<const char*>(w), bias, residual, y, pre, ntiles);
   };
-  if (gated(x.act)) return go(RowsTile<true>());
-  return go(RowsTile<false>());
+  if (gated(x.act)) return go(Type<RowsTile<true>>());
+  return go(Type<RowsTile<false>>());
 }
 
 hipError_t launch_expert_rows_grad(const ExpertDims& x, const int32_t* off, const uint16_t* gz,
                                    const uint16_t* w, uint16_t* gx, hipStream_t s) {
   using P = RowsGradTile;
-  const TileGrid<P::BM, P::BN> grid(1, x.rows / P::BM + x.E, ceil_div(x.K, P::BN));
-  return in_ranges(grid.blocks(), [&](dim3 blocks, int64_t b) {
-    return launch(MOE_KERNEL_EXPERT_ROWS_GRAD, expert_rows_grad_kernel<P>, blocks, dim3(P::kThreads), 0,
-                  s, x, off, reinterpret_cast<const char*>(gz), reinterpret_cast<const char*>(w), gx,
-                  grid, b);
-  });
+  const int ntiles = ceil_div(x.K, P::BN);
+  return launch(MOE_KERNEL_EXPERT_ROWS_GRAD, expert_rows_grad_kernel<P>, row_blocks<P>(x, ntiles),
+                dim3(P::kThreads), 0, s, x, off, reinterpret_cast<const char*>(gz),
+                reinterpret_cast<const char*>(w), gx, ntiles);
 }
 
 hipError_t launch_expert_wgrad(const ExpertDims& x, const int32_t* off, const uint16_t* gz,
                                const uint16_t* a, void* gw, bool f32, hipStream_t s) {
   using P = WgradTile;
   const TileGrid<P::BM, P::BN> grid(x.E, ceil_div(x.Z, P::BM), ceil_div(x.K, P::BN));
-  return in_ranges(grid.blocks(), [&](dim3 blocks, int64_t b) {
-    return launch(MOE_KERNEL_EXPERT_WGRAD, f32 ? expert_wgrad_kernel<P, true> : expert_wgrad_kernel<P, false>,
-                  blocks, dim3(P::kThreads), 0, s, x, off, reinterpret_cast<const char*>(gz),
-                  reinterpret_cast<const char*>(a), gw, grid, b);
-  });
+  return launch(MOE_KERNEL_EXPERT_WGRAD,
+                f32 ? expert_wgrad_kernel<P, true> : expert_wgrad_kernel<P, false>,
+                dim3(std::min(grid.numbers(), blocks_at_once<P>())), dim3(P::kThreads), 0, s, x, off,
+                reinterpret_cast<const char*>(gz), reinterpret_cast<const char*>(a), gw, grid);
 }
 
 hipError_t launch_expert_act_grad(const ExpertDims& x, const int32_t* off, const uint16_t* gy,
