@@ -721,6 +721,120 @@ __global__ __launch_bounds__(P::kThreads, 2) void expert_rows_kernel(
   }
 }
 
+// ---- rows of few tokens: the same product where an expert has a few rows
+
+// Decoding: every used expert's weights are read once for a handful of rows,
+// so the product is bound by that read and needs many loads under way rather
+// than tiles.  One block computes 16 columns of y (of gate and up, when gated)
+// for one expert; its waves split the contraction, read weights and rows
+// straight into matrix-instruction registers, kFewSteps steps (32 values each)
+// at a time, and add their parts through LDS in a fixed order.  MT * 16 rows a
+// pass; an expert with more takes further passes, which find the weights in L2.
+constexpr int kFewWaves = 4;
+constexpr int kFewSteps = 8;
+
+template <int MT, bool GATED>
+__global__ __launch_bounds__(kFewWaves * kWave) void expert_few_rows_kernel(
+    ExpertDims x, const int32_t* __restrict__ off, const char* __restrict__ a,
+    const char* __restrict__ w, const float* __restrict__ bias,
+    const uint16_t* __restrict__ residual, uint16_t* __restrict__ y, uint16_t* __restrict__ pre,
+    int strips) {
+  constexpr int H = GATED ? 2 : 1;
+  __shared__ float part[kFewWaves][MT * H][256];
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int which = blockIdx.x / strips, col0 = blockIdx.x % strips * 16;
+  int e = which;
+  if (x.rows < x.E) {
+    // Fewer rows than experts: `which` is a row, and the block of its expert's
+    // first row does the work.
+    const int step = (x.E + kWave - 1) / kWave;
+    const int e1 = lane * step;
+    e = (__popcll(__ballot(e1 < x.E && off[min(e1, x.E)] <= which)) - 1) * step;
+    if (step > 1) {
+      const int e2 = e + lane;
+      e += __popcll(__ballot(lane < step && e2 < x.E && off[min(e2, x.E)] <= which)) - 1;
+    }
+    e = __builtin_amdgcn_readfirstlane(e);
+    if (off[e] != which) return;
+  }
+  const int o0 = off[e], rows = off[e + 1] - o0;
+  const uint32_t ld = (uint32_t)x.K * 2;
+  const int steps = (x.K + 31) / 32;
+  const int first = wave * steps / kFewWaves, last = (wave + 1) * steps / kFewWaves;
+  const int i = lane & 15, g = lane >> 4;
+  const __amdgpu_buffer_rsrc_t rw = uniform_buffer(w + (int64_t)e * x.Z * ld, (uint32_t)x.Z * ld);
+  // (col0 + i may be past the last column: such rows of w give results that are not stored, or
+  // are past the descriptor's end.)
+  const uint32_t vw = (uint32_t)(col0 + i) * ld + g * 16, up = (uint32_t)x.N * ld;
+  for (int r0 = 0; r0 < rows; r0 += MT * 16) {
+    const __amdgpu_buffer_rsrc_t rx = uniform_buffer(
+        a + (int64_t)(o0 + r0) * ld, (uint32_t)min(rows - r0, MT * 16) * ld);  // rows past the end: zeros
+    f32x4 acc[MT][H];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < H; ++h) acc[m][h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = first; s < last; s += kFewSteps) {
+      bf16x8 fw[kFewSteps][H], fx[kFewSteps][MT];
+#pragma unroll
+      for (int q = 0; q < kFewSteps; ++q) {
+        // Steps past this wave's part and chunks past the row's end read zeros.
+        const bool in = s + q < last && (s + q) * 32 + g * 8 < x.K;
+        const uint32_t k = (uint32_t)(s + q) * 64;
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+          fw[q][h] = __builtin_bit_cast(
+              bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rw, in ? vw + h * up + k : kPast, 0, 0));
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          fx[q][m] = __builtin_bit_cast(
+              bf16x8, __builtin_amdgcn_raw_buffer_load_b128(
+                          rx, in ? (uint32_t)(m * 16 + i) * ld + g * 16 + k : kPast, 0, 0));
+      }
+#pragma unroll
+      for (int q = 0; q < kFewSteps; ++q)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            acc[m][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[q][h], fx[q][m], acc[m][h], 0, 0, 0);
+    }
+    // acc[m][h][q]: column g * 4 + q, row m * 16 + i.
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+        *reinterpret_cast<f32x4*>(&part[wave][m * H + h][i * 16 + g * 4]) = acc[m][h];
+    __syncthreads();
+    for (int t = threadIdx.x; t < MT * 256; t += kFewWaves * kWave) {
+      const int m = t / 256, r = r0 + m * 16 + t % 256 / 16, col = col0 + t % 16;
+      if (r >= rows || col >= x.N) continue;
+      float z[H];
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        z[h] = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kFewWaves; ++q) z[h] += part[q][m * H + h][t % 256];
+        if (bias != nullptr) z[h] += bias[(int64_t)e * x.Z + h * x.N + col];
+      }
+      const int64_t row = o0 + r;
+      float out[8] = {z[0]};
+      if (pre != nullptr) {
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+          pre[row * x.Z + h * x.N + col] = (uint16_t)bf16_pair(z[h], 0.0f);
+      }
+      act_values(x.act, out);
+      if constexpr (GATED) out[0] *= z[1];
+      if (residual != nullptr)
+        out[0] += __uint_as_float((uint32_t)residual[row * x.N + col] << 16);
+      y[row * x.N + col] = (uint16_t)bf16_pair(out[0], 0.0f);
+    }
+    __syncthreads();
+  }
+}
+
 // ---- rows grad: gx = gz w
 
 template <typename P>
@@ -958,6 +1072,22 @@ hipError_t in_ranges(int64_t total, F f) {
 
 constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+// The kernel for few rows is taken up to kFewRows rows an expert on average,
+// and up to twice that where the tiles would leave more than half of the CUs
+// without one.  Its passes take 16 rows up to half of kFewRows (or where no
+// expert can have more), else 32.  Measured, few rows against tiles, 2048 ->
+// 1024: gated, 64 experts, top-8: 1 token 13.3 and 29.5 us, 16 tokens 85.9 and
+// 112.8, 64 tokens 116.5 and 125.5, 128 tokens 134.4 and 126.5; not gated, 8
+// experts, top-2, 64 tokens 12.0 and 29.7; 16 rows a pass against 32: 64
+// experts, 32 tokens 98.4 and 102.3 us.
+constexpr int kFewRows = 8;
+
+bool few_rows(const ExpertDims& x) {
+  const int64_t most = (int64_t)x.E * kFewRows;
+  const int tiles = ceil_div(x.N, gated(x.act) ? 128 : 256);
+  return x.rows <= most || (x.rows <= 2 * most && (int64_t)x.E * tiles <= kCus / 2);
+}
+
 // Blocks for the row products: the most row tiles there can be are
 // rows / BM + E (the counts are only known on the device).
 template <typename P>
@@ -981,6 +1111,18 @@ using WgradTile = TileProduct<128, 256, 1, 4, true, true, false>;
 hipError_t launch_expert_rows(const ExpertDims& x, const int32_t* off, const uint16_t* a,
                               const uint16_t* w, const float* bias, const uint16_t* residual,
                               uint16_t* y, uint16_t* pre, hipStream_t s) {
+  auto few = [&](auto kernel) {
+    const int strips = ceil_div(x.N, 16);
+    return launch(MOE_KERNEL_EXPERT_FEW_ROWS, kernel,
+                  dim3((uint32_t)std::min(x.E, x.rows) * (uint32_t)strips), dim3(kFewWaves * kWave), 0,
+                  s, x, off, reinterpret_cast<const char*>(a), reinterpret_cast<const char*>(w), bias,
+                  residual, y, pre, strips);
+  };
+  if (few_rows(x)) {
+    if (x.T <= 16 || (int64_t)x.rows <= (int64_t)x.E * (kFewRows / 2))
+      return gated(x.act) ? few(expert_few_rows_kernel<1, true>) : few(expert_few_rows_kernel<1, false>);
+    return gated(x.act) ? few(expert_few_rows_kernel<2, true>) : few(expert_few_rows_kernel<2, false>);
+  }
   auto go = [&](auto tile) {
     using P = typename decltype(tile)::type;
     const int ntiles = ceil_div(x.N, P::GATED ? P::BN / 2 : P::BN);

@@ -159,6 +159,9 @@ EXPERTS = [
     (1, 8, 2, 64, 64, "uniform"),
     (2, 40, 8, 136, 72, "uniform"),
     (16, 16, 4, 512, 256, "uniform"),
+    (16, 200, 3, 1000, 40, "uniform"),
+    (13, 6, 2, 2056, 24, "few"),
+    (100, 60, 4, 96, 88, "skewed"),
     (63, 4, 2, 72, 200, "bad"),
     (65, 100, 6, 1000, 328, "uniform"),
     (300, 7, 3, 264, 520, "uniform"),
@@ -525,11 +528,13 @@ def test_given_stream_is_used(dev):
 
 
 def test_timing_names_every_launch(dev):
-    m = Layer(300, 264, 136, 12, 4, 3, dev, seed=5)
-    m.plan.timing(64)
-    m.step()
-    names = {n for n, _, ms in m.plan.timing_read() if ms > 0}
-    m.plan.timing(0)
+    names = set()
+    for T in (4, 300):   # few rows an expert, and many
+        m = Layer(T, 264, 136, 12, 4, 3, dev, seed=5)
+        m.plan.timing(64)
+        m.step()
+        names |= {n for n, _, ms in m.plan.timing_read() if ms > 0}
+        m.plan.timing(0)
     assert {_abi.kernel_name(i) for i in range(22, _abi.KERNEL_COUNT)} <= names
 
 

@@ -141,7 +141,8 @@ def test_backward_workspace_bytes():
 def test_kernel_names():
     names = [_abi.kernel_name(i) for i in range(22, _abi.KERNEL_COUNT)]
     assert names == ["router_kernel", "router_grad_kernel", "dispatch_grad_kernel",
-                     "combine_grad_kernel", "expert_rows_kernel", "expert_rows_grad_kernel",
+                     "combine_grad_kernel", "expert_rows_kernel", "expert_few_rows_kernel",
+                     "expert_rows_grad_kernel",
                      "expert_wgrad_kernel", "expert_act_grad_kernel", "expert_bias_sum_kernel"]
 
 
