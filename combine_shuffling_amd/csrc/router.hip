@@ -3,10 +3,9 @@
 //
 // One wave per token; lane l holds the logits of experts i * 64 + l, so the
 // row is read once, coalesced, and stays in registers.  Choice: every key
-// becomes one unsigned 64-bit number, the key's float order above the
-// complement of the expert id, so the largest number is the largest key with
-// ties to the lower id and no two numbers are equal; k rounds of a wave-wide
-// maximum give the ids in descending order.
+// becomes an unsigned number of the same order; k rounds find the largest
+// with a wave-wide maximum of data-parallel moves, and the lowest expert that
+// holds it with a ballot for each i.
 //
 // Weights: with p the softmax or the sigmoid, a renormalised weight is
 // p_j / sum_i p_i over the selected = exp(l_j - m) / sum_i exp(l_i - m) with
@@ -49,25 +48,70 @@ __device__ __forceinline__ uint32_t key_bits(float v) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-#pragma unroll
-  for (int s = 32; s > 0; s >>= 1) {
-    const uint64_t o = __shfl_xor(v, s);
-    v = o > v ? o : v;
+// v in another lane of the row of 16 (or of the rows before), `other` where
+// there is none: data-parallel moves, no LDS.
+constexpr int kRowShr = 0x110, kBcast15 = 0x142, kBcast31 = 0x143;
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ uint32_t moved(uint32_t other, uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)other, (int)v, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ float moved(float other, float v) {
+  return __uint_as_float(moved<CTRL, ROWS>(__float_as_uint(other), __float_as_uint(v)));
+}
+
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
+// Folds f over the first 16 lanes (into lane 15) or all 64 (into lane 63) and
+// gives every lane the result.  The order is fixed.
+template <bool WHOLE, typename T, typename F>
+__device__ __forceinline__ T fold(T v, T none, F f) {
+  v = f(v, moved<kRowShr + 1>(none, v));
+  v = f(v, moved<kRowShr + 2>(none, v));
+  v = f(v, moved<kRowShr + 4>(none, v));
+  v = f(v, moved<kRowShr + 8>(none, v));
+  if constexpr (WHOLE) {
+    v = f(v, moved<kBcast15, 0xa>(none, v));
+    v = f(v, moved<kBcast31, 0xc>(none, v));
   }
-  return v;
+  constexpr int last = WHOLE ? kWave - 1 : 15;
+  if constexpr (std::is_same_v<T, float>)
+    return lane_value(v, last);
+  else
+    return (T)__builtin_amdgcn_readlane((int)v, last);
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int s = 32; s > 0; s >>= 1) v = fmaxf(v, __shfl_xor(v, s));
-  return v;
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+template <bool WHOLE>
+__device__ __forceinline__ float fold_max(float v) {
+  return fold<WHOLE>(v, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
+template <bool WHOLE>
+__device__ __forceinline__ float fold_sum(float v) {
+  return fold<WHOLE>(v, 0.0f, [](float a, float b) { return a + b; });
+}
+
+// The entry with the largest key, the lowest number first: entry i * 64 + lane
+// is key[i].  Sets its key to 0 (no entry).
+template <int V>
+__device__ __forceinline__ int take_largest(uint32_t (&key)[V]) {
+  uint32_t best = key[0];
 #pragma unroll
-  for (int s = 32; s > 0; s >>= 1) v += __shfl_xor(v, s);
-  return v;
+  for (int i = 1; i < V; ++i) best = larger(best, key[i]);
+  best = fold<true>(best, 0u, larger);
+  int found = -1;
+#pragma unroll
+  for (int i = V - 1; i >= 0; --i) {
+    const uint64_t at = __ballot(key[i] == best);
+    found = at != 0 ? i * kWave + __builtin_ctzll(at) : found;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) key[i] = found == i * kWave + (int)(threadIdx.x % kWave) ? 0u : key[i];
+  return found;
 }
 
 // exp(x - m) for x <= m, with exp(inf - inf) = 1 (the limit of equal logits)
@@ -90,9 +134,9 @@ __device__ __forceinline__ float selected_score(const moe_router_config& c, floa
                                                 float row_max, float row_sum) {
   if (c.renormalise) {
     const float l = !has ? -INFINITY : c.score == MOE_SCORE_SIGMOID ? log_sigmoid(x) : x;
-    const float m = wave_max(l);
+    const float m = fold_max<false>(l);
     const float e = exp_below(l, m);
-    const float sum = wave_sum(e);
+    const float sum = fold_sum<false>(e);
     return sum > 0.0f ? e / sum : 0.0f;
   }
   if (!has) return 0.0f;
@@ -106,85 +150,79 @@ __global__ __launch_bounds__(kRouterWaves * kWave) void router_kernel(
     Dims d, moe_router_config c, const void* __restrict__ logits, const float* __restrict__ bias,
     int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
   __shared__ float s_key[kRouterWaves][V * kWave];
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   for (int64_t t = (int64_t)blockIdx.x * kRouterWaves + wave; t < d.T;
        t += (int64_t)gridDim.x * kRouterWaves) {
     float x[V], v[V];
-    uint64_t key[V];
+    uint32_t key[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = i * kWave + lane;
       x[i] = e < d.E ? load_logit<F32>(logits, t * d.E + e) : -INFINITY;
       v[i] = bias != nullptr && e < d.E ? x[i] + bias[e] : x[i];
-      key[i] = e < d.E ? (uint64_t)key_bits(v[i]) << 32 | (uint32_t)~e : 0;
+      key[i] = e < d.E ? key_bits(v[i]) : 0;
     }
     if (c.nodes_per_token > 0) {
-      // Lane n sums node n's two largest keys (its experts are consecutive).
-      // The waves of a block use their own part of s_key and do not wait for
-      // each other, only for their own writes.
+      // The largest two keys of each node: `share` lanes scan a node's
+      // consecutive experts and join what they found.  The waves of a block
+      // use their own part of s_key and do not wait for each other, only for
+      // their own writes.
 #pragma unroll
-      for (int i = 0; i < V; ++i) s_key[wave][i * kWave + lane] = v[i];
+      for (int i = 0; i < V; ++i) s_key[wave][i * kWave + lane] = no_nan(v[i]);
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      uint64_t node = 0;
-      if (lane < d.N) {
-        const int r0 = lane * d.G, r1 = r0 + d.G;
-        const int e0 = r0 * d.ebase + min(r0, d.erem), e1 = r1 * d.ebase + min(r1, d.erem);
-        float a = -INFINITY, b = -INFINITY;
-        for (int e = e0; e < e1; ++e) {
-          const float q = no_nan(s_key[wave][e]);
-          b = fmaxf(b, fminf(a, q));
-          a = fmaxf(a, q);
-        }
-        // two opposite infinities: the larger one decides
-        const float worth = e1 - e0 < 2 || a == INFINITY ? a : a + b;
-        node = (uint64_t)key_bits(worth) << 32 | (uint32_t)~lane;
+      int share = kWave;
+      while (share * d.N > kWave) share >>= 1;
+      const int n = lane / share;
+      const int r0 = min(n, d.N) * d.G, r1 = min(n + 1, d.N) * d.G;
+      const int e0 = r0 * d.ebase + min(r0, d.erem), e1 = r1 * d.ebase + min(r1, d.erem);
+      float a = -INFINITY, b = -INFINITY;
+      for (int e = e0 + lane % share; e < e1; e += share) {
+        const float q = s_key[wave][e];
+        b = fmaxf(b, fminf(a, q));
+        a = fmaxf(a, q);
       }
-      uint64_t kept = 0;  // bit n: node n may be chosen
+      for (int s = share >> 1; s > 0; s >>= 1) {
+        const float a2 = __shfl_xor(a, s), b2 = __shfl_xor(b, s);
+        b = fmaxf(fmaxf(b, b2), fminf(a, a2));
+        a = fmaxf(a, a2);
+      }
+      // two opposite infinities: the larger one decides
+      const float worth = e1 - e0 < 2 || a == INFINITY ? a : a + b;
+      uint32_t node[1] = {n < d.N && lane % share == 0 ? key_bits(worth) : 0};
+      bool kept[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) kept[i] = false;
       for (int m = 0; m < c.nodes_per_token; ++m) {
-        const uint64_t best = wave_max(node);
-        const int n = (int)~(uint32_t)best;
-        kept |= 1ull << (n & 63);
-        if (lane == n) node = 0;
+        const int k0 = take_largest(node) / share * d.G, k1 = k0 + d.G;
+        const int f0 = k0 * d.ebase + min(k0, d.erem), f1 = k1 * d.ebase + min(k1, d.erem);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          kept[i] = kept[i] || (i * kWave + lane >= f0 && i * kWave + lane < f1);
       }
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = i * kWave + lane;
-        if (e < d.E && !(kept >> (split_part(e, d.ebase, d.erem) / d.G) & 1)) key[i] = 0;
-      }
+      for (int i = 0; i < V; ++i) key[i] = kept[i] ? key[i] : 0;
       __builtin_amdgcn_wave_barrier();  // the next token's keys overwrite s_key
     }
-    int id = 0;      // lane j (< k): the j-th expert
-    float xs = 0.0f;  // and its logit
+    int id = 0;  // lane j (< k): the j-th expert
     for (int j = 0; j < d.k; ++j) {
-      uint64_t best = key[0];
-#pragma unroll
-      for (int i = 1; i < V; ++i) best = key[i] > best ? key[i] : best;
-      best = wave_max(best);
-      const int e = (int)~(uint32_t)best;
-      if (lane == j) id = e;
-      float mine = 0.0f;
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (key[i] == best) {
-          key[i] = 0;
-          mine = x[i];
-        }
-      const float got = __shfl(mine, e & (kWave - 1));
-      if (lane == j) xs = got;
+      const int e = take_largest(key);
+      id = lane == j ? e : id;
     }
+    const bool has = lane < d.k;
+    const float xs = has ? load_logit<F32>(logits, t * d.E + id) : 0.0f;
     float row_max = 0.0f, row_sum = 0.0f;
     if (c.score == MOE_SCORE_SOFTMAX && !c.renormalise) {
       row_max = -INFINITY;
 #pragma unroll
       for (int i = 0; i < V; ++i) row_max = fmaxf(row_max, no_nan(x[i]));
-      row_max = wave_max(row_max);
+      row_max = fold_max<true>(row_max);
 #pragma unroll
       for (int i = 0; i < V; ++i) row_sum += exp_below(no_nan(x[i]), row_max);
-      row_sum = wave_sum(row_sum);
+      row_sum = fold_sum<true>(row_sum);
     }
-    const bool has = lane < d.k;
     const float p = selected_score(c, no_nan(xs), has, row_max, row_sum);
     if (has) {
       topk_idx[t * d.k + lane] = id;
@@ -204,7 +242,8 @@ __global__ __launch_bounds__(kRouterWaves * kWave) void router_grad_kernel(
     Dims d, moe_router_config c, const void* __restrict__ logits,
     const int32_t* __restrict__ topk_idx, const float* __restrict__ grad_w,
     void* __restrict__ grad_logits) {
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const bool whole = c.score == MOE_SCORE_SOFTMAX && !c.renormalise;
   for (int64_t t = (int64_t)blockIdx.x * kRouterWaves + wave; t < d.T;
        t += (int64_t)gridDim.x * kRouterWaves) {
@@ -226,20 +265,20 @@ __global__ __launch_bounds__(kRouterWaves * kWave) void router_grad_kernel(
         p[i] = e < d.E ? no_nan(load_logit<F32>(logits, t * d.E + e)) : -INFINITY;
         row_max = fmaxf(row_max, p[i]);
       }
-      row_max = wave_max(row_max);
+      row_max = fold_max<true>(row_max);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         p[i] = exp_below(p[i], row_max);
         row_sum += p[i];
       }
-      row_sum = wave_sum(row_sum);
+      row_sum = fold_sum<true>(row_sum);
       const float inv = row_sum > 0.0f ? 1.0f / row_sum : 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) p[i] *= inv;
     }
     const float ps = selected_score(c, xs, has, row_max, row_sum);
     float gj = 0.0f, dot = 0.0f;  // this lane's entry of the gradient
-    if (c.renormalise || whole) dot = wave_sum(has ? ps * g : 0.0f);
+    if (c.renormalise || whole) dot = fold_sum<false>(has ? ps * g : 0.0f);
     if (c.renormalise) {
       gj = ps * (g - dot);
       if (c.score == MOE_SCORE_SIGMOID) gj *= 1.0f / (1.0f + expf(xs));  // 1 - sigmoid(xs)
@@ -254,7 +293,7 @@ __global__ __launch_bounds__(kRouterWaves * kWave) void router_grad_kernel(
     for (int i = 0; i < V; ++i) out[i] = whole ? -p[i] * dot : 0.0f;
     for (int j = 0; j < d.k; ++j) {
       const int e = __builtin_amdgcn_readlane(id, j);
-      const float a = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(gj), j));
+      const float a = lane_value(gj, j);
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (e == i * kWave + lane) out[i] += a;
