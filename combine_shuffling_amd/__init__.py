@@ -64,6 +64,9 @@ def _ptr(t: torch.Tensor | None) -> ctypes.c_void_p:
 
 
 def _need(t: torch.Tensor, shape, dtypes, name: str, device) -> None:
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and
+            t.device == device and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -96,26 +99,8 @@ def _out(t: torch.Tensor | None, shape, dtype, name: str, device) -> torch.Tenso
     return t
 
 
-class _On:
-    """Makes `device` the current one where it is not (a kernel is launched on
-    the current device)."""
-
-    def __init__(self, device: torch.device):
-        self.device = device
-        self.prev = None
-
-    def __enter__(self):
-        if self.device.type != "cuda":
-            raise ValueError(f"tensors must be on the GPU, not on {self.device}")
-        now = torch.cuda.current_device()
-        if self.device.index is not None and now != self.device.index:
-            self.prev = now
-            torch.cuda.set_device(self.device)
-
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            torch.cuda.set_device(self.prev)
-        return False
+def _addr(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
 
 
 class Plan:
@@ -154,6 +139,23 @@ class Plan:
         if h is not None and h.value:
             self._lib.moe_plan_destroy(h)
             self._h = None
+
+    def _launch(self, name: str, device: torch.device, stream, *args) -> None:
+        """Calls the library's `name` on this plan with the stream last, with `device` current
+        (a kernel is launched on the current device)."""
+        if device.type != "cuda":
+            raise ValueError(f"tensors must be on the GPU, not on {device}")
+        # The raw handle: making a torch.cuda.Stream object takes 2 us, a sixth of a small call.
+        handle = (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
+                  else stream.cuda_stream)
+        fn = getattr(self._lib, name)
+        if device.index == torch.cuda.current_device():
+            st = fn(self._h, *args, handle)
+        else:
+            with torch.cuda.device(device):
+                st = fn(self._h, *args, handle)
+        if st != _abi.OK:
+            raise MoeError(st, name)
 
     # -- moe_route_plan
     def route(self, topk_idx: torch.Tensor, workspace: torch.Tensor | None = None, stream=None):
@@ -333,7 +335,8 @@ class Plan:
     def _router_config(self, score: str, renormalise: bool, nodes_per_token: int, scale: float):
         if score not in _abi.SCORE:
             raise ValueError(f"score must be one of {tuple(_abi.SCORE)}")
-        return _abi.RouterConfig(_abi.SCORE[score], int(bool(renormalise)), nodes_per_token, scale)
+        return ctypes.byref(_abi.RouterConfig(_abi.SCORE[score], bool(renormalise), nodes_per_token,
+                                              scale))
 
     def router(self, logits: torch.Tensor, bias: torch.Tensor | None = None,
                score: str = "softmax", renormalise: bool = True, scale: float = 1.0,
@@ -350,13 +353,10 @@ class Plan:
         if bias is not None:
             _need(bias, (self.E,), _F32, "bias", dev)
         cfg = self._router_config(score, renormalise, nodes_per_token, scale)
-        with _On(dev):
-            topk_idx = _out(topk_idx, (self.T, self.k), torch.int32, "topk_idx", dev)
-            topk_w = _out(topk_w, (self.T, self.k), torch.float32, "topk_w", dev)
-            _abi.check(self._lib.moe_router(self._h, ctypes.byref(cfg), _ptr(logits),
-                                            _OUT_CODE[logits.dtype], _ptr(bias), _ptr(topk_idx),
-                                            _ptr(topk_w), _stream_handle(dev, stream)),
-                       "moe_router")
+        topk_idx = _out(topk_idx, (self.T, self.k), torch.int32, "topk_idx", dev)
+        topk_w = _out(topk_w, (self.T, self.k), torch.float32, "topk_w", dev)
+        self._launch("moe_router", dev, stream, cfg, logits.data_ptr(), _OUT_CODE[logits.dtype],
+                     _addr(bias), topk_idx.data_ptr(), topk_w.data_ptr())
         return topk_idx, topk_w
 
     # -- moe_router_backward
@@ -370,12 +370,10 @@ class Plan:
         _need(topk_idx, (self.T, self.k), (torch.int32,), "topk_idx", dev)
         _need(grad_w, (self.T, self.k), _F32, "grad_w", dev)
         cfg = self._router_config(score, renormalise, 0, scale)
-        with _On(dev):
-            grad_logits = _out(grad_logits, (self.T, self.E), logits.dtype, "grad_logits", dev)
-            _abi.check(self._lib.moe_router_backward(
-                self._h, ctypes.byref(cfg), _ptr(logits), _OUT_CODE[logits.dtype], _ptr(topk_idx),
-                _ptr(grad_w), _ptr(grad_logits), _stream_handle(dev, stream)),
-                "moe_router_backward")
+        grad_logits = _out(grad_logits, (self.T, self.E), logits.dtype, "grad_logits", dev)
+        self._launch("moe_router_backward", dev, stream, cfg, logits.data_ptr(),
+                     _OUT_CODE[logits.dtype], topk_idx.data_ptr(), grad_w.data_ptr(),
+                     grad_logits.data_ptr())
         return grad_logits
 
     # -- moe_dispatch_backward
@@ -387,11 +385,9 @@ class Plan:
             raise MoeError(_abi.ERR_PLAN_NOT_ROUTED, "dispatch_backward")
         _need(grad_recv, (self.recv_rows, self.H), _BF16_LIKE, "grad_recv", dev)
         code = _out_code(out_dtype, "out_dtype")
-        with _On(dev):
-            grad_x = _out(grad_x, (self.T, self.H), out_dtype, "grad_x", dev)
-            _abi.check(self._lib.moe_dispatch_backward(self._h, _ptr(grad_recv), _ptr(grad_x), code,
-                                                       _stream_handle(dev, stream)),
-                       "moe_dispatch_backward")
+        grad_x = _out(grad_x, (self.T, self.H), out_dtype, "grad_x", dev)
+        self._launch("moe_dispatch_backward", dev, stream, grad_recv.data_ptr(), grad_x.data_ptr(),
+                     code)
         return grad_x
 
     # -- moe_combine_backward
@@ -406,12 +402,11 @@ class Plan:
         _need(grad_out, (self.T, self.H), (torch.float32, torch.bfloat16), "grad_out", dev)
         _need(y, (self.recv_rows, self.H), _BF16_LIKE, "y", dev)
         _need(topk_w, (self.T, self.k), _F32, "topk_w", dev)
-        with _On(dev):
-            grad_y = _out(grad_y, (self.recv_rows, self.H), torch.bfloat16, "grad_y", dev)
-            grad_w = _out(grad_w, (self.T, self.k), torch.float32, "grad_w", dev)
-            _abi.check(self._lib.moe_combine_backward(
-                self._h, _ptr(grad_out), _OUT_CODE[grad_out.dtype], _ptr(y), _ptr(topk_w),
-                _ptr(grad_y), _ptr(grad_w), _stream_handle(dev, stream)), "moe_combine_backward")
+        grad_y = _out(grad_y, (self.recv_rows, self.H), torch.bfloat16, "grad_y", dev)
+        grad_w = _out(grad_w, (self.T, self.k), torch.float32, "grad_w", dev)
+        self._launch("moe_combine_backward", dev, stream, grad_out.data_ptr(),
+                     _OUT_CODE[grad_out.dtype], y.data_ptr(), topk_w.data_ptr(), grad_y.data_ptr(),
+                     grad_w.data_ptr())
         return grad_y, grad_w
 
     # -- moe_expert_linear
@@ -430,7 +425,7 @@ class Plan:
                 raise ValueError("a gated activation needs an even number of weight rows")
             N = Z // 2
         _need(w, (self.E, Z, K), _BF16, "w", self.device)
-        return _abi.ExpertConfig(K, N, _abi.ACTIVATION[activation]), K, N, Z
+        return ctypes.byref(_abi.ExpertConfig(K, N, _abi.ACTIVATION[activation])), K, N, Z
 
     def expert_linear(self, x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
                       residual: torch.Tensor | None = None, activation: str = "none",
@@ -452,13 +447,11 @@ class Plan:
             _need(bias, (self.E, Z), _F32, "bias", dev)
         if residual is not None:
             _need(residual, (rows, N), _BF16, "residual", dev)
-        with _On(dev):
-            y = _out(y, (rows, N), torch.bfloat16, "y", dev)
-            if save_pre or pre is not None:
-                pre = _out(pre, (rows, Z), torch.bfloat16, "pre", dev)
-            _abi.check(self._lib.moe_expert_linear(
-                self._h, ctypes.byref(cfg), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(y),
-                _ptr(pre), _stream_handle(dev, stream)), "moe_expert_linear")
+        y = _out(y, (rows, N), torch.bfloat16, "y", dev)
+        if save_pre or pre is not None:
+            pre = _out(pre, (rows, Z), torch.bfloat16, "pre", dev)
+        self._launch("moe_expert_linear", dev, stream, cfg, x.data_ptr(), w.data_ptr(), _addr(bias),
+                     _addr(residual), y.data_ptr(), _addr(pre))
         return y, pre
 
     # -- moe_expert_linear_backward
@@ -486,19 +479,17 @@ class Plan:
         else:
             pre = None
         code = _out_code(grad_w_dtype, "grad_w_dtype")
-        need = int(self._lib.moe_expert_backward_workspace_bytes(self._h, ctypes.byref(cfg)))
+        need = self._lib.moe_expert_backward_workspace_bytes(self._h, cfg)
         if workspace is not None and workspace.numel() * workspace.element_size() < need:
             raise ValueError("workspace too small")
-        with _On(dev):
-            if workspace is None:
-                workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-            grad_x = torch.empty((rows, K), dtype=torch.bfloat16, device=dev) if x_grad else None
-            grad_w = torch.empty((self.E, Z, K), dtype=grad_w_dtype, device=dev) if w_grad else None
-            grad_b = torch.empty((self.E, Z), dtype=torch.float32, device=dev) if bias_grad else None
-            _abi.check(self._lib.moe_expert_linear_backward(
-                self._h, ctypes.byref(cfg), _ptr(grad_y), _ptr(x), _ptr(w), _ptr(pre), _ptr(grad_x),
-                _ptr(grad_w), code, _ptr(grad_b), _ptr(workspace), _stream_handle(dev, stream)),
-                "moe_expert_linear_backward")
+        if workspace is None:
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        grad_x = torch.empty((rows, K), dtype=torch.bfloat16, device=dev) if x_grad else None
+        grad_w = torch.empty((self.E, Z, K), dtype=grad_w_dtype, device=dev) if w_grad else None
+        grad_b = torch.empty((self.E, Z), dtype=torch.float32, device=dev) if bias_grad else None
+        self._launch("moe_expert_linear_backward", dev, stream, cfg, grad_y.data_ptr(), x.data_ptr(),
+                     w.data_ptr(), _addr(pre), _addr(grad_x), _addr(grad_w), code, _addr(grad_b),
+                     workspace.data_ptr())
         return grad_x, grad_w, grad_b
 
     # -- moe_plan_timing / moe_plan_timing_read
