@@ -37,7 +37,6 @@ namespace moe {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -70,6 +69,11 @@ __device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) r[q] = bf16_pair(f[2 * q], f[2 * q + 1]);
   return r;
+}
+
+__device__ __forceinline__ u32x4 pack_two(f32x4 lo, f32x4 hi) {
+  return u32x4{bf16_pair(lo[0], lo[1]), bf16_pair(lo[2], lo[3]), bf16_pair(hi[0], hi[1]),
+               bf16_pair(hi[2], hi[3])};
 }
 
 __device__ __forceinline__ uint32_t uniform(uint32_t v) {
@@ -321,39 +325,44 @@ struct TileProduct {
   static constexpr int kLds = kStages * kStage;
   static constexpr int QA = kABytes / 1024 / kNW, QB = kBBytes / 1024 / kNW;  // loads a wave and stage
   static_assert(QA * kNW * 1024 == kABytes && QB * kNW * 1024 == kBBytes);
-  static_assert(BT || TN == 64, "the permuted columns of a wave are 64 wide");
+  static_assert(TN == 64, "the order of a wave's columns is of 64");
 
+  // Columns of B.  A lane gets four consecutive result columns of each of a
+  // wave's four fragments; lane group g (of four) is given columns
+  // 32 (j / 2) + 8 g + 4 (j % 2) + 0..3 of the wave's 64 for fragment j, so that two
+  // fragments make 16 bytes of bf16 and the four groups 64 consecutive bytes
+  // of a result row.  (Stores that cover less of a line cost the most where
+  // results outweigh operands: with 32 bytes a row and the streaming hint,
+  // which keeps L2 from joining them, the weight gradient of a Zipf batch took
+  // 1250 us instead of 830.)
+  //
   // Contiguous contraction: LDS row r (64 bytes, 4 chunks) holds chunk
-  // p ^ swizzle(r) at position p.  A's rows are read in order; B's in the
-  // order of the permuted columns (rows i % 4 + 16 * (i / 4) for lane i), so
-  // each has the swizzle that spreads its own eight consecutive lanes over
-  // all banks.
+  // p ^ swizzle(r) at position p.  A's rows are read in order, B's in the order
+  // above (rows i % 4 + 8 (i / 4) for lane i); each has the swizzle that spreads
+  // its own eight consecutive lanes over all banks.
   template <bool B>
   static __device__ __forceinline__ int swizzle(int r) {
-    return B ? ((r >> 1) & 1) | ((r >> 4) & 1) << 1 : (r >> 1) & 3;
+    return B ? ((r >> 1) & 1) | ((r >> 3) & 1) << 1 : (r >> 1) & 3;
   }
-  // Transposed: LDS row kr (along the contraction) of W columns; the 32-byte
-  // block b of a row sits at position b ^ spread(kr).
-  template <int W>
+  // Transposed: LDS row kr (along the contraction) holds W columns in units of
+  // 16 bytes; unit u is at position u ^ spread(kr).
   static __device__ __forceinline__ int spread(int kr) {
-    return ((kr & 3) | ((kr >> 3) & 3) << 2) & (W / 16 - 1);
+    return (kr & 3) << 2 | ((kr >> 3) & 1) << 1;
   }
   // Byte offset in memory of a lane's 16 bytes for the wave's q-th load.
   template <int W>
   static __device__ __forceinline__ uint32_t offset_t(uint32_t ld, int wave, int lane, int q) {
-    constexpr int per = W / 8;       // 16-byte positions a row
+    constexpr int per = W / 8;       // units a row
     const int pos = (q * kNW + wave) * 64 + lane;
     const int kr = pos / per, p = pos % per;
-    return kr * ld + ((((p >> 1) ^ spread<W>(kr)) << 1) | (p & 1)) * 16;
+    return kr * ld + (p ^ spread(kr)) * 16;
   }
 
-  // Memory row of B's LDS row r.  Gated: a wave's 64 rows are 32 of the gate
-  // and 32 of the up projection, in the order that puts 8 consecutive columns
-  // of both into one lane.
+  // Memory row of B's LDS row r.  Gated: a wave's first 32 rows are of the
+  // gate, the other 32 the same columns of the up projection.
   static __device__ __forceinline__ int b_row(int r, int gate_up) {
     if constexpr (!GATED) return r;
-    const int slab = r / 64, q = (r >> 4) & 3, jj = (r >> 2) & 3;
-    return slab * 32 + q * 8 + (jj & 1) * 4 + (r & 3) + (jj >> 1) * gate_up;
+    return r / 64 * 32 + (r & 31) + ((r >> 5) & 1) * gate_up;
   }
 
   struct Fragments {
@@ -555,28 +564,28 @@ struct TileProduct {
                                                in ? v[q] : kPast, 0, 0, 0);
   }
 
+  // This lane's part of fragment f of an operand whose wave starts at `first`.
   template <bool T, bool B, int W>
   static __device__ __forceinline__ bf16x8 fragment(const char* tile, int first, int f, int lane) {
     const int i = lane & 15, g = lane >> 4;
     if constexpr (T) {
-      const int kr = g * 8 + (i >> 2);
-      const char* p = tile + kr * (W * 2) + (((first / 16 + f) ^ spread<W>(kr)) << 5) + (i & 3) * 8;
+      // Lane i names 4 columns (8 bytes) of row i / 4 and gets column i of four rows.
+      const int kr = g * 8 + (i >> 2), piece = i & 3;
+      const int col = first + (B ? f / 2 * 32 + piece * 8 + f % 2 * 4 : f * 16 + piece * 4);
+      const char* p = tile + kr * (W * 2) + (((col >> 3) ^ spread(kr)) << 4) + (col & 4) * 2;
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)p);
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(p + 4 * W * 2));
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      const int r = B ? first + (i >> 2) * 16 + f * 4 + (i & 3) : first + f * 16 + i;
+      const int r = first + (B ? f / 2 * 32 + (i >> 2) * 8 + f % 2 * 4 + (i & 3) : f * 16 + i);
       const char* p = tile + r * 64 + ((g ^ swizzle<B>(r)) << 4);
       return *reinterpret_cast<const bf16x8*>(p);
     }
   }
 };
 
-// A lane of acc[i][j] holds result row (first row of the wave) + i * 16 + lane % 16
-// and four consecutive columns, lane / 16 * 4 + 0..3 of the fragment.  In the
-// row product the fragment's columns are spread so that a lane's NJ * 4
-// columns are consecutive: lane / 16 * 16 + j * 4 + 0..3 of the wave's 64
-// (gated: lane / 16 * 8 + (j & 1) * 4 of its 32, j >> 1 the gate or up).
+// A lane of acc[i][j] holds four results of row m0 + i * WM * 16 + lane % 16 of
+// the tile, in the columns described above.
 
 // Blocks of a launch: each CU gets as many as fit its LDS, and every block
 // computes one tile after another (numbers blockIdx.x, + gridDim.x, ...).
@@ -611,7 +620,7 @@ __device__ __forceinline__ void rows_epilogue(const P& p, const ExpertDims& x, c
 #pragma unroll
       for (int h = 0; h < kHalves; ++h)
         res[i][h] = *reinterpret_cast<const u32x4*>(residual + row[i] * x.N +
-                                                    (c0 + h * 8 < x.N ? c0 + h * 8 : 0));
+                                                    (c0 + h * 32 < x.N ? c0 + h * 32 : 0));
   }
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
@@ -626,7 +635,7 @@ __device__ __forceinline__ void rows_epilogue(const P& p, const ExpertDims& x, c
     if (!ok[i]) continue;
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
-      const int col = c0 + h * 8;
+      const int col = c0 + h * 32;
       if (col >= x.N) continue;
       float out[8];
 #pragma unroll
@@ -695,14 +704,14 @@ __global__ __launch_bounds__(P::kThreads, 2) void expert_rows_kernel(
     p.run(c, next, P::steps_of(x.K), s.rows);
 
     const int g = p.lane >> 4;
-    const int c0 = col0 + p.wave % P::WN * (P::GATED ? 32 : 64) + g * (P::GATED ? 8 : 16);
+    const int c0 = col0 + p.wave % P::WN * (P::GATED ? 32 : 64) + g * 8;
     float bz[16];
 #pragma unroll
     for (int q = 0; q < 16; ++q) bz[q] = 0.0f;
     if (bias != nullptr) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int col = P::GATED ? c0 : c0 + h * 8;
+        const int col = P::GATED ? c0 : c0 + h * 32;
         if (col < x.N) {
           const f32x4* q = reinterpret_cast<const f32x4*>(bias + (int64_t)s.e * x.Z + col +
                                                           (P::GATED ? h * x.N : 0));
@@ -875,18 +884,17 @@ __global__ __launch_bounds__(P::kThreads, 2) void expert_rows_grad_kernel(
     const int col0 = n_ahead;
     p.run(c, next, P::steps_of(x.Z), s.rows);
 
-    const int c0 = col0 + p.n0 + (p.lane >> 4) * 4;
+    const int c0 = col0 + p.n0 + (p.lane >> 4) * 8;
 #pragma unroll
     for (int i = 0; i < P::MI; ++i) {
       const int m = p.m0 + i * (P::WM * 16) + (p.lane & 15);
       if (m >= s.rows) continue;
 #pragma unroll
-      for (int j = 0; j < P::NJ; ++j) {
-        const int col = c0 + j * 16;
+      for (int h = 0; h < 2; ++h) {
+        const int col = c0 + h * 32;
         if (col >= x.K) continue;
-        const f32x4 v = p.acc[i][j];
-        *reinterpret_cast<u32x2*>(gx + (int64_t)(s.row + m) * x.K + col) =
-            u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+        *reinterpret_cast<u32x4*>(gx + (int64_t)(s.row + m) * x.K + col) =
+            pack_two(p.acc[i][2 * h], p.acc[i][2 * h + 1]);
       }
     }
   }
@@ -929,22 +937,24 @@ __global__ __launch_bounds__(P::kThreads, 2) void expert_wgrad_kernel(
     p.run(c, next, P::steps_of(c.len), x.Z - t.m * P::BM);
 
     const int r0 = t.m * P::BM + p.m0 + (p.lane & 15);
-    const int c0 = t.n * P::BN + p.n0 + (p.lane >> 4) * 4;
+    const int c0 = t.n * P::BN + p.n0 + (p.lane >> 4) * 8;
 #pragma unroll
     for (int i = 0; i < P::MI; ++i) {
       const int m = r0 + i * (P::WM * 16);
       if (m >= x.Z) continue;
 #pragma unroll
-      for (int j = 0; j < P::NJ; ++j) {
-        const int col = c0 + j * 16;
+      for (int h = 0; h < 2; ++h) {
+        const int col = c0 + h * 32;
         if (col >= x.K) continue;
-        const f32x4 v = p.acc[i][j];
+        const f32x4 lo = p.acc[i][2 * h], hi = p.acc[i][2 * h + 1];
         const int64_t at = ((int64_t)t.grid * x.Z + m) * x.K + col;
-        if constexpr (F32)
-          *reinterpret_cast<f32x4*>(static_cast<float*>(gw) + at) = v;
-        else
-          *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(gw) + at) =
-              u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+        if constexpr (F32) {
+          f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(gw) + at);
+          o[0] = lo;
+          o[1] = hi;
+        } else {
+          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(gw) + at) = pack_two(lo, hi);
+        }
       }
     }
   }
@@ -1104,7 +1114,8 @@ struct Type {
 template <bool GATED>
 using RowsTile = TileProduct<256, 256, 2, 4, false, false, GATED>;
 using RowsGradTile = TileProduct<128, 256, 1, 4, false, true, false>;
-using WgradTile = TileProduct<128, 256, 1, 4, true, true, false>;
+template <int BM, int WM>
+using WgradTile = TileProduct<BM, 256, WM, 4, true, true, false>;
 
 }  // namespace
 
@@ -1145,12 +1156,20 @@ hipError_t launch_expert_rows_grad(const ExpertDims& x, const int32_t* off, cons
 
 hipError_t launch_expert_wgrad(const ExpertDims& x, const int32_t* off, const uint16_t* gz,
                                const uint16_t* a, void* gw, bool f32, hipStream_t s) {
-  using P = WgradTile;
-  const TileGrid<P::BM, P::BN> grid(x.E, ceil_div(x.Z, P::BM), ceil_div(x.K, P::BN));
-  return launch(MOE_KERNEL_EXPERT_WGRAD,
-                f32 ? expert_wgrad_kernel<P, true> : expert_wgrad_kernel<P, false>,
-                dim3(std::min(grid.numbers(), blocks_at_once<P>())), dim3(P::kThreads), 0, s, x, off,
-                reinterpret_cast<const char*>(gz), reinterpret_cast<const char*>(a), gw, grid);
+  auto go = [&](auto tile) {
+    using P = typename decltype(tile)::type;
+    const TileGrid<P::BM, P::BN> grid(x.E, ceil_div(x.Z, P::BM), ceil_div(x.K, P::BN));
+    return launch(MOE_KERNEL_EXPERT_WGRAD,
+                  f32 ? expert_wgrad_kernel<P, true> : expert_wgrad_kernel<P, false>,
+                  dim3(std::min(grid.numbers(), blocks_at_once<P>())), dim3(P::kThreads), 0, s, x, off,
+                  reinterpret_cast<const char*>(gz), reinterpret_cast<const char*>(a), gw, grid);
+  };
+  // Large tiles where every CU gets at least four of them (64 experts, 4096
+  // tokens, top-8, 2048 x 2048: 347 us against 365; 1021 tokens, 1000 x 776, 480 tiles:
+  // 23.4 us against 22.6; one expert of 32768 rows, 64 tiles: 745 against 497).
+  const int64_t tiles = (int64_t)x.E * ceil_div(x.Z, 256) * ceil_div(x.K, 256);
+  if (tiles >= 4 * kCus) return go(Type<WgradTile<256, 2>>());
+  return go(Type<WgradTile<128, 1>>());
 }
 
 hipError_t launch_expert_act_grad(const ExpertDims& x, const int32_t* off, const uint16_t* gy,
