@@ -24,21 +24,26 @@ hipError_t launch_combine_grad(const Dims& d, const void* grad_out, bool f32, co
                                const float* wts, uint16_t* grad_y, float* grad_w, const Work& w,
                                hipStream_t s);
 
-// expert.hip.  Sizes of one expert product: `rows` receive rows (T * k) sorted
-// by expert, off[E + 1] the experts' first rows; K in, N out, Z = the width of
-// the product itself.
+// expert.hip.  Sizes of one expert product: `rows` receive rows (T * k), sorted
+// by expert inside each band, off[b * (E + 1) + e] the experts' first rows (of
+// all bands together, in order); K in, N out, Z = the width of the product
+// itself.
 struct ExpertDims {
   int32_t rows, E, K, N, Z;
   int32_t T;              // tokens: no expert has more rows
   int32_t act;            // moe_activation
+  int32_t bands;          // 1: not banded
+  int32_t band_tokens;    // tokens a band (the last may have fewer)
 };
 inline bool gated(int32_t act) { return act == MOE_ACT_SWIGLU || act == MOE_ACT_GEGLU; }
 
-// Rows per slot of the partial bias sums, and the slots: expert e's slots
-// start at off[e] / kBiasRows + e, which leaves room for the rows of every
-// expert without knowing their counts on the host.
+// Rows per slot of the partial bias sums, and the slots: expert e's of band b
+// start at off / kBiasRows + e + b * E (off: its first row), which leaves room
+// for the rows of every expert without knowing their counts on the host.
 constexpr int kBiasRows = 64;
-inline int64_t bias_slots(const ExpertDims& x) { return x.rows / kBiasRows + x.E; }
+inline int64_t bias_slots(const ExpertDims& x) {
+  return x.rows / kBiasRows + (int64_t)x.bands * x.E;
+}
 
 hipError_t launch_expert_rows(const ExpertDims& x, const int32_t* off, const uint16_t* a,
                               const uint16_t* w, const float* bias, const uint16_t* residual,

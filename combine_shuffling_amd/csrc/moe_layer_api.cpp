@@ -48,8 +48,8 @@ moe_status expert_dims(const moe_plan* plan, const moe_expert_config* c, ExpertD
   const int64_t Z = (int64_t)c->out_features * (gated(c->activation) ? 2 : 1);
   if (c->in_features > kMaxFeatures || Z > kMaxFeatures || Z * c->in_features >= kMaxWeight)
     return MOE_ERR_UNSUPPORTED;
-  if (d.nbands > 1) return MOE_ERR_UNSUPPORTED;
-  *out = ExpertDims{d.T * d.k, d.E, c->in_features, c->out_features, (int32_t)Z, d.T, c->activation};
+  *out = ExpertDims{d.T * d.k, d.E,           c->in_features, c->out_features, (int32_t)Z,
+                    d.T,       c->activation, d.nbands,       d.band};
   return MOE_OK;
 }
 

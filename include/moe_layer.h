@@ -123,10 +123,10 @@ typedef struct moe_expert_config {
  *   pre[r] = z[r] rounded to bf16         (kept for the gradient)
  * x: [T*k, K] bf16; w: [E, Z, K] bf16; bias: [E, Z] float32 or NULL; residual:
  * [T*k, N] bf16 or NULL; y: [T*k, N] bf16; pre: [T*k, Z] bf16 or NULL.
- * K and N are the product's own (not the plan's H).  Not for banded plans.
- * Limits: E * K * Z and T*k * max(K, Z) any; Z * K < 2^30, K and Z <= 2^20.
- * Errors: PLAN_NOT_ROUTED, INVALID_ARGUMENT, UNSUPPORTED (banded plan, sizes
- * beyond the limits), HIP. */
+ * K and N are the product's own (not the plan's H).  Banded plans are computed
+ * band by band, a launch each.  Limits: Z * K < 2^30, K and Z <= 2^20.
+ * Errors: PLAN_NOT_ROUTED, INVALID_ARGUMENT, UNSUPPORTED (sizes beyond the
+ * limits), HIP. */
 moe_status moe_expert_linear(moe_plan* plan, const moe_expert_config* cfg, const uint16_t* x,
                              const uint16_t* w, const float* bias, const uint16_t* residual,
                              uint16_t* y, uint16_t* pre, void* stream);

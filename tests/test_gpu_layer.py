@@ -300,14 +300,42 @@ def test_empty_batch(dev):
     assert idx.shape == wt.shape == (0, 2)
 
 
-def test_expert_linear_refuses_bands_and_wide_weights(dev):
-    plan = cs.Plan(512, 64, 4, 2, 1, band_tokens=256)
-    plan.route(torch.zeros(512, 2, dtype=torch.int32, device=dev) +
-               torch.arange(2, dtype=torch.int32, device=dev))
-    with pytest.raises(cs.MoeError) as e:
-        plan.expert_linear(torch.zeros(1024, 64, dtype=torch.bfloat16, device=dev),
-                           torch.zeros(4, 64, 64, dtype=torch.bfloat16, device=dev))
-    assert e.value.status == _abi.ERR_UNSUPPORTED
+@pytest.mark.parametrize("T,band,E,k,K,N,act", [
+    (1000, 256, 6, 2, 136, 72, "swiglu"),     # bands that end inside the slots of bias sums
+    (700, 256, 60, 3, 72, 264, "gelu"),
+    (1300, 512, 3, 2, 264, 520, "none"),
+    (260, 256, 40, 1, 64, 64, "silu"),        # a last band of fewer rows than experts
+])
+def test_expert_products_on_banded_plans(T, band, E, k, K, N, act, dev):
+    say(f"[layer] banded experts T={T} band={band} E={E} k={k} K={K} N={N} {act}")
+    rng = np.random.default_rng(T + N)
+    idx, _, x, w, b, gy = expert_inputs(rng, T, E, k, K, N, "uniform", act)
+    idx[5, 0] = -1          # a dropped slot: the band's last row stays as it is
+    plan = routed(idx, E, 1, 64, dev, band_tokens=band)
+    Z = w.shape[1]
+    pre = rounded(rng.normal(size=(T * k, Z))) if act != "none" else None
+    xd, wd, gd = bf16(x, dev), bf16(w, dev), bf16(gy, dev)
+    full = torch.full((T * k, N), 7.0, dtype=torch.bfloat16, device=dev)
+    y, _ = plan.expert_linear(xd, wd, torch.from_numpy(b.astype(np.float32)).to(dev), None, act, y=full)
+    gx, gw, gb = plan.expert_linear_backward(gd, xd, wd, None if pre is None else bf16(pre, dev), act,
+                                             bias_grad=True, grad_w_dtype=torch.float32)
+    offs = plan.read("expert_offsets").reshape(-1, E + 1)
+    assert np.array_equal(offs[:, 0], np.arange(len(offs)) * band * k)
+    total = {n: [0.0, 0.0] for n in ("grad_w", "grad_bias")}
+    for o in offs:
+        s = slice(o[0], o[-1])
+        local = o - o[0]
+        want, ey, _, _ = ref.expert_linear(x[s], w, b, None, act, local)
+        check(y[s], want, ey, "y")
+        r = ref.expert_linear_backward(gy[s], x[s], w, None if pre is None else pre[s], act, local)
+        check(gx[s], *r["grad_x"], "grad_x")
+        for n, t in total.items():
+            t[0], t[1] = t[0] + r[n][0], t[1] + r[n][1]
+    # the bands' sums are added up in float32: their number more roundings of the magnitudes
+    for n, got in (("grad_w", gw), ("grad_bias", gb)):
+        check(got, total[n][0], total[n][1] * (1 + len(offs)), n)
+    hole = offs[0][-1]
+    assert hole == band * k - 1 and (y[hole] == 7).all()
 
 
 # ---- the router

@@ -118,15 +118,6 @@ def test_expert_config_refusals(cfg, want):
     assert L.moe_expert_backward_workspace_bytes(p._h, ctypes.byref(c)) == 0
 
 
-def test_expert_products_refuse_banded_plans():
-    p = plan(T=1024, band_tokens=256)
-    c = _abi.ExpertConfig(64, 64, 0)
-    assert _abi.lib().moe_expert_linear(p._h, ctypes.byref(c), vp(16), vp(16), None, None, vp(16),
-                                        None, None) == UNSUPPORTED
-    assert _abi.lib().moe_expert_linear(p._h, None, vp(16), vp(16), None, None, vp(16), None,
-                                        None) == BAD
-
-
 def test_backward_workspace_bytes():
     # grad_z (with an activation) and 64-row partial sums of every column
     p = plan(T=100, E=8, k=2)
@@ -136,6 +127,10 @@ def test_backward_workspace_bytes():
     assert size(64, 64, 0) == slots * 64 * 4
     assert size(64, 64, 4) == 200 * 128 * 2 + slots * 128 * 4
     assert size(64, 40, 2) % 256 == 0
+    # banded: every band has slots of its own for its experts
+    p = plan(T=1024, band_tokens=256)
+    assert size(64, 64, 0) == (2048 // 64 + 4 * 8) * 64 * 4
+    assert L.moe_expert_linear(p._h, None, vp(16), vp(16), None, None, vp(16), None, None) == BAD
 
 
 def test_kernel_names():
