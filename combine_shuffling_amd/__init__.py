@@ -35,6 +35,7 @@ the layer's gradients:
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import numpy as np
 import torch
@@ -103,6 +104,18 @@ def _addr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+def _on_stream(method):
+    """A call that also takes stream=: it then runs with that stream current, so that what it
+    allocates belongs to that stream too."""
+    @functools.wraps(method)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return method(*args, **kw)
+        with torch.cuda.stream(stream):
+            return method(*args, **kw)
+    return call
+
+
 class Plan:
     """Owns one moe_plan (host) and, once routed, its device workspace tensor."""
 
@@ -140,20 +153,19 @@ class Plan:
             self._lib.moe_plan_destroy(h)
             self._h = None
 
-    def _launch(self, name: str, device: torch.device, stream, *args) -> None:
-        """Calls the library's `name` on this plan with the stream last, with `device` current
-        (a kernel is launched on the current device)."""
+    def _launch(self, name: str, device: torch.device, *args) -> None:
+        """Calls the library's `name` on this plan and the device's current stream, with `device`
+        current (a kernel is launched on the current device)."""
         if device.type != "cuda":
             raise ValueError(f"tensors must be on the GPU, not on {device}")
         # The raw handle: making a torch.cuda.Stream object takes 2 us, a sixth of a small call.
-        handle = (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
-                  else stream.cuda_stream)
+        stream = torch._C._cuda_getCurrentRawStream(device.index)
         fn = getattr(self._lib, name)
         if device.index == torch.cuda.current_device():
-            st = fn(self._h, *args, handle)
+            st = fn(self._h, *args, stream)
         else:
             with torch.cuda.device(device):
-                st = fn(self._h, *args, handle)
+                st = fn(self._h, *args, stream)
         if st != _abi.OK:
             raise MoeError(st, name)
 
@@ -338,10 +350,11 @@ class Plan:
         return ctypes.byref(_abi.RouterConfig(_abi.SCORE[score], bool(renormalise), nodes_per_token,
                                               scale))
 
+    @_on_stream
     def router(self, logits: torch.Tensor, bias: torch.Tensor | None = None,
                score: str = "softmax", renormalise: bool = True, scale: float = 1.0,
                nodes_per_token: int = 0, topk_idx: torch.Tensor | None = None,
-               topk_w: torch.Tensor | None = None, stream=None):
+               topk_w: torch.Tensor | None = None):
         """Gate logits [T, E] (float32 or bf16) -> (topk_idx int32 [T, k], topk_w float32 [T, k]).
 
         The k experts of the largest logit + bias (bias: float32 [E], for the choice only), in
@@ -355,14 +368,15 @@ class Plan:
         cfg = self._router_config(score, renormalise, nodes_per_token, scale)
         topk_idx = _out(topk_idx, (self.T, self.k), torch.int32, "topk_idx", dev)
         topk_w = _out(topk_w, (self.T, self.k), torch.float32, "topk_w", dev)
-        self._launch("moe_router", dev, stream, cfg, logits.data_ptr(), _OUT_CODE[logits.dtype],
+        self._launch("moe_router", dev, cfg, logits.data_ptr(), _OUT_CODE[logits.dtype],
                      _addr(bias), topk_idx.data_ptr(), topk_w.data_ptr())
         return topk_idx, topk_w
 
     # -- moe_router_backward
+    @_on_stream
     def router_backward(self, logits: torch.Tensor, topk_idx: torch.Tensor, grad_w: torch.Tensor,
                         score: str = "softmax", renormalise: bool = True, scale: float = 1.0,
-                        grad_logits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                        grad_logits: torch.Tensor | None = None) -> torch.Tensor:
         """Gradient of the weights with respect to the logits (the choice fixed): [T, E], every
         entry written, of the logits' dtype."""
         dev = logits.device
@@ -371,14 +385,15 @@ class Plan:
         _need(grad_w, (self.T, self.k), _F32, "grad_w", dev)
         cfg = self._router_config(score, renormalise, 0, scale)
         grad_logits = _out(grad_logits, (self.T, self.E), logits.dtype, "grad_logits", dev)
-        self._launch("moe_router_backward", dev, stream, cfg, logits.data_ptr(),
+        self._launch("moe_router_backward", dev, cfg, logits.data_ptr(),
                      _OUT_CODE[logits.dtype], topk_idx.data_ptr(), grad_w.data_ptr(),
                      grad_logits.data_ptr())
         return grad_logits
 
     # -- moe_dispatch_backward
+    @_on_stream
     def dispatch_backward(self, grad_recv: torch.Tensor, grad_x: torch.Tensor | None = None,
-                          out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+                          out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
         """Gradient of dispatch: grad_x[t] = sum_j grad_recv[slot_of[t, j]], [T, H]."""
         dev = self.device
         if dev is None:
@@ -386,14 +401,14 @@ class Plan:
         _need(grad_recv, (self.recv_rows, self.H), _BF16_LIKE, "grad_recv", dev)
         code = _out_code(out_dtype, "out_dtype")
         grad_x = _out(grad_x, (self.T, self.H), out_dtype, "grad_x", dev)
-        self._launch("moe_dispatch_backward", dev, stream, grad_recv.data_ptr(), grad_x.data_ptr(),
+        self._launch("moe_dispatch_backward", dev, grad_recv.data_ptr(), grad_x.data_ptr(),
                      code)
         return grad_x
 
     # -- moe_combine_backward
+    @_on_stream
     def combine_backward(self, grad_out: torch.Tensor, y: torch.Tensor, topk_w: torch.Tensor,
-                         grad_y: torch.Tensor | None = None, grad_w: torch.Tensor | None = None,
-                         stream=None):
+                         grad_y: torch.Tensor | None = None, grad_w: torch.Tensor | None = None):
         """Gradient of combine and combine_hier: returns (grad_y [T*k, H] bf16 in the receive
         layout, grad_w [T, k] float32); grad_out: [T, H] bf16 or float32."""
         dev = self.device
@@ -404,7 +419,7 @@ class Plan:
         _need(topk_w, (self.T, self.k), _F32, "topk_w", dev)
         grad_y = _out(grad_y, (self.recv_rows, self.H), torch.bfloat16, "grad_y", dev)
         grad_w = _out(grad_w, (self.T, self.k), torch.float32, "grad_w", dev)
-        self._launch("moe_combine_backward", dev, stream, grad_out.data_ptr(),
+        self._launch("moe_combine_backward", dev, grad_out.data_ptr(),
                      _OUT_CODE[grad_out.dtype], y.data_ptr(), topk_w.data_ptr(), grad_y.data_ptr(),
                      grad_w.data_ptr())
         return grad_y, grad_w
@@ -427,10 +442,11 @@ class Plan:
         _need(w, (self.E, Z, K), _BF16, "w", self.device)
         return ctypes.byref(_abi.ExpertConfig(K, N, _abi.ACTIVATION[activation])), K, N, Z
 
+    @_on_stream
     def expert_linear(self, x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
                       residual: torch.Tensor | None = None, activation: str = "none",
                       save_pre: bool = False, y: torch.Tensor | None = None,
-                      pre: torch.Tensor | None = None, stream=None):
+                      pre: torch.Tensor | None = None):
         """Every expert's product on its rows of the receive layout: returns (y, pre).
 
         y[r] = act(x[r] . w[e]^T + bias[e]) + residual[r] for each receive row r of expert e;
@@ -450,21 +466,26 @@ class Plan:
         y = _out(y, (rows, N), torch.bfloat16, "y", dev)
         if save_pre or pre is not None:
             pre = _out(pre, (rows, Z), torch.bfloat16, "pre", dev)
-        self._launch("moe_expert_linear", dev, stream, cfg, x.data_ptr(), w.data_ptr(), _addr(bias),
+        self._launch("moe_expert_linear", dev, cfg, x.data_ptr(), w.data_ptr(), _addr(bias),
                      _addr(residual), y.data_ptr(), _addr(pre))
         return y, pre
 
     # -- moe_expert_linear_backward
+    @_on_stream
     def expert_linear_backward(self, grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
                                pre: torch.Tensor | None = None, activation: str = "none",
                                bias_grad: bool = False, x_grad: bool = True, w_grad: bool = True,
                                grad_w_dtype: torch.dtype = torch.bfloat16,
-                               workspace: torch.Tensor | None = None, stream=None):
+                               grad_x: torch.Tensor | None = None,
+                               grad_w: torch.Tensor | None = None,
+                               grad_bias: torch.Tensor | None = None,
+                               workspace: torch.Tensor | None = None):
         """Gradient of expert_linear: returns (grad_x [T*k, K] bf16, grad_w [E, Z, K] of
         grad_w_dtype, grad_bias [E, Z] float32), None for one that is not wanted.
 
-        pre: what expert_linear stored, needed with an activation.  The gradient of the residual
-        is grad_y."""
+        pre: what expert_linear stored, needed with an activation.  x_grad, w_grad, bias_grad say
+        which are wanted; grad_x, grad_w, grad_bias: tensors to write them to.  The gradient of the
+        residual is grad_y."""
         dev = self.device
         if dev is None:
             raise MoeError(_abi.ERR_PLAN_NOT_ROUTED, "expert_linear_backward")
@@ -484,13 +505,13 @@ class Plan:
             raise ValueError("workspace too small")
         if workspace is None:
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        grad_x = torch.empty((rows, K), dtype=torch.bfloat16, device=dev) if x_grad else None
-        grad_w = torch.empty((self.E, Z, K), dtype=grad_w_dtype, device=dev) if w_grad else None
-        grad_b = torch.empty((self.E, Z), dtype=torch.float32, device=dev) if bias_grad else None
-        self._launch("moe_expert_linear_backward", dev, stream, cfg, grad_y.data_ptr(), x.data_ptr(),
-                     w.data_ptr(), _addr(pre), _addr(grad_x), _addr(grad_w), code, _addr(grad_b),
+        grad_x = _out(grad_x, (rows, K), torch.bfloat16, "grad_x", dev) if x_grad else None
+        grad_w = _out(grad_w, (self.E, Z, K), grad_w_dtype, "grad_w", dev) if w_grad else None
+        grad_bias = _out(grad_bias, (self.E, Z), torch.float32, "grad_bias", dev) if bias_grad else None
+        self._launch("moe_expert_linear_backward", dev, cfg, grad_y.data_ptr(), x.data_ptr(),
+                     w.data_ptr(), _addr(pre), _addr(grad_x), _addr(grad_w), code, _addr(grad_bias),
                      workspace.data_ptr())
-        return grad_x, grad_w, grad_b
+        return grad_x, grad_w, grad_bias
 
     # -- moe_plan_timing / moe_plan_timing_read
     def timing(self, capacity: int) -> None:
@@ -586,7 +607,7 @@ def router(plan: Plan, logits: torch.Tensor, bias=None, score: str = "softmax",
            topk_w=None, stream=None):
     """moe_router: returns (topk_idx [T, k] int32, topk_w [T, k] float32)."""
     return plan.router(logits, bias, score, renormalise, scale, nodes_per_token, topk_idx, topk_w,
-                       stream)
+                       stream=stream)
 
 
 def router_backward(plan: Plan, logits: torch.Tensor, topk_idx: torch.Tensor, grad_w: torch.Tensor,
@@ -594,31 +615,34 @@ def router_backward(plan: Plan, logits: torch.Tensor, topk_idx: torch.Tensor, gr
                     grad_logits=None, stream=None) -> torch.Tensor:
     """moe_router_backward: returns grad_logits [T, E]."""
     return plan.router_backward(logits, topk_idx, grad_w, score, renormalise, scale, grad_logits,
-                                stream)
+                                stream=stream)
 
 
 def dispatch_backward(plan: Plan, grad_recv: torch.Tensor, grad_x=None,
                       out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """moe_dispatch_backward: returns grad_x [T, H] (bf16 or float32)."""
-    return plan.dispatch_backward(grad_recv, grad_x, out_dtype, stream)
+    return plan.dispatch_backward(grad_recv, grad_x, out_dtype, stream=stream)
 
 
 def combine_backward(plan: Plan, grad_out: torch.Tensor, y: torch.Tensor, topk_w: torch.Tensor,
                      grad_y=None, grad_w=None, stream=None):
     """moe_combine_backward: returns (grad_y [T*k, H] bf16, grad_w [T, k] float32)."""
-    return plan.combine_backward(grad_out, y, topk_w, grad_y, grad_w, stream)
+    return plan.combine_backward(grad_out, y, topk_w, grad_y, grad_w, stream=stream)
 
 
 def expert_linear(plan: Plan, x: torch.Tensor, w: torch.Tensor, bias=None, residual=None,
                   activation: str = "none", save_pre: bool = False, y=None, pre=None, stream=None):
     """moe_expert_linear: returns (y [T*k, N] bf16, pre [T*k, Z] bf16 or None)."""
-    return plan.expert_linear(x, w, bias, residual, activation, save_pre, y, pre, stream)
+    return plan.expert_linear(x, w, bias, residual, activation, save_pre, y, pre,
+                              stream=stream)
 
 
 def expert_linear_backward(plan: Plan, grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
                            pre=None, activation: str = "none", bias_grad: bool = False,
                            x_grad: bool = True, w_grad: bool = True,
-                           grad_w_dtype: torch.dtype = torch.bfloat16, workspace=None, stream=None):
+                           grad_w_dtype: torch.dtype = torch.bfloat16, grad_x=None, grad_w=None,
+                           grad_bias=None, workspace=None, stream=None):
     """moe_expert_linear_backward: returns (grad_x, grad_w, grad_bias), None where not wanted."""
     return plan.expert_linear_backward(grad_y, x, w, pre, activation, bias_grad, x_grad, w_grad,
-                                       grad_w_dtype, workspace, stream)
+                                       grad_w_dtype, grad_x, grad_w, grad_bias, workspace,
+                                       stream=stream)

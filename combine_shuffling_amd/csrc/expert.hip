@@ -751,12 +751,13 @@ __global__ __launch_bounds__(kFewWaves * kWave) void expert_few_rows_kernel(
     ExpertDims x, const int32_t* __restrict__ off, const char* __restrict__ a,
     const char* __restrict__ w, const float* __restrict__ bias,
     const uint16_t* __restrict__ residual, uint16_t* __restrict__ y, uint16_t* __restrict__ pre,
-    int strips) {
+    int strips, int64_t base) {
   constexpr int H = GATED ? 2 : 1;
   __shared__ float part[kFewWaves][MT * H][256];
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int which = blockIdx.x / strips, col0 = blockIdx.x % strips * 16;
+  const int64_t block = base + blockIdx.x;
+  const int which = (int)(block / strips), col0 = (int)(block % strips) * 16;
   int e = which;
   if (x.rows < x.E) {
     // Fewer rows than experts: `which` is a row (of the band), and the block of
@@ -1012,7 +1013,7 @@ __global__ __launch_bounds__(kActCols * kActRows) void expert_act_grad_kernel(
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        if (r + i * kActRows >= s.rows) break;
+        if (r + i * kActRows >= s.rows) continue;
         const int64_t row = s.row + r + i * kActRows;
         float g[8], o[8];
         unpack8(vg[i], g);
@@ -1083,8 +1084,7 @@ __global__ __launch_bounds__(256) void expert_bias_sum_kernel(ExpertDims x,
   gb[(int64_t)e * x.Z + n] = t;
 }
 
-// Launches `total` blocks in ranges of at most kMaxTileBlocks (a multiple of
-// the XCDs, so that a block keeps its XCD).
+// Launches `total` blocks in ranges of at most kMaxTileBlocks.
 template <typename F>
 hipError_t in_ranges(int64_t total, F f) {
   hipError_t e = hipSuccess;
@@ -1154,10 +1154,11 @@ hipError_t expert_rows(const ExpertDims& x, const int32_t* off, const uint16_t* 
                        uint16_t* pre, hipStream_t s) {
   auto few = [&](auto kernel) {
     const int strips = ceil_div(x.N, 16);
-    return launch(MOE_KERNEL_EXPERT_FEW_ROWS, kernel,
-                  dim3((uint32_t)std::min(x.E, x.rows) * (uint32_t)strips), dim3(kFewWaves * kWave), 0,
-                  s, x, off, reinterpret_cast<const char*>(a), reinterpret_cast<const char*>(w), bias,
-                  residual, y, pre, strips);
+    return in_ranges((int64_t)std::min(x.E, x.rows) * strips, [&](dim3 blocks, int64_t b) {
+      return launch(MOE_KERNEL_EXPERT_FEW_ROWS, kernel, blocks, dim3(kFewWaves * kWave), 0, s, x, off,
+                    reinterpret_cast<const char*>(a), reinterpret_cast<const char*>(w), bias, residual,
+                    y, pre, strips, b);
+    });
   };
   if (few_rows(x)) {
     if (x.T <= 16 || (int64_t)x.rows <= (int64_t)x.E * (kFewRows / 2))

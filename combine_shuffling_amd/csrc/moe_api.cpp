@@ -110,9 +110,16 @@ Work bind_work(const Layout& l, void* base) {
 }
 
 moe_status ensure_scanned(moe_plan* plan, hipStream_t s) {
-  if (plan->scanned) return MOE_OK;
+  if (plan->scanned && !plan->d.fused_scan && plan->scan_capture == 0) return MOE_OK;
+  hipStreamCaptureStatus capturing = hipStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (hipStreamGetCaptureInfo(s, &capturing, &id) != hipSuccess) return MOE_ERR_HIP;
+  if (capturing != hipStreamCaptureStatusActive) id = 0;
+  if (plan->scanned && (plan->scan_capture == id || (plan->scan_capture == 0 && !plan->d.fused_scan)))
+    return MOE_OK;
   if (launch_route_scan(plan->d, plan->work, s) != hipSuccess) return MOE_ERR_HIP;
   plan->scanned = true;
+  plan->scan_capture = id;
   return MOE_OK;
 }
 
@@ -237,6 +244,7 @@ moe_status moe_plan_create(const moe_config* cfg, moe_plan** out) {
   p->ws = nullptr;
   p->routed = false;
   p->scanned = false;
+  p->scan_capture = 0;
   p->assigned = false;
   p->timer = nullptr;
   *out = p;
@@ -395,6 +403,7 @@ moe_status moe_pipeline(moe_plan* plan, const int32_t* topk_idx, void* workspace
     return MOE_ERR_HIP;
   plan->routed = true;
   plan->scanned = true;
+  plan->scan_capture = 0;
   plan->assigned = true;
   return MOE_OK;
 }

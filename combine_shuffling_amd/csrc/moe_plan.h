@@ -27,6 +27,7 @@ struct moe_plan {
   moe::Work work;
   bool routed;     // route_count has been launched for the bound routing
   bool scanned;    // route_scan has been launched for it (tile bases, offsets, status)
+  unsigned long long scan_capture;  // the stream capture that recorded it (0: none, it has run)
   bool assigned;   // slot_of / row_src (and stage_of / stage_src) are final
   moe::LaunchTimer* timer;  // per-launch timing, or null
 };
@@ -49,6 +50,9 @@ struct TimerScope {
 };
 
 // Launches the plan's scan if the route left it to the gather (small plans).
+// A scan recorded into a graph counts in that capture only; and a capture on a
+// plan whose route leaves the scan out records one, so that a graph replayed
+// after another route of the plan reads that route's offsets.
 moe_status ensure_scanned(moe_plan* plan, hipStream_t s);
 // Makes slot_of / row_src (and the staging arrays) final when no dispatch
 // has done it since the last route.

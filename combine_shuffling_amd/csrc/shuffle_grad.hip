@@ -95,8 +95,8 @@ __global__ __launch_bounds__(kCombineGradWaves * kWave) void combine_grad_kernel
   __shared__ float s_dot[kCombineGradWaves][KMAX];
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
   const uint32_t rows = (uint32_t)(d.T * d.k);
-  for (int t = blockIdx.x; t < d.T; t += gridDim.x) {
-    const int64_t at = (int64_t)t * d.k;
+  for (int64_t t = blockIdx.x; t < d.T; t += gridDim.x) {
+    const int64_t at = t * d.k;
     int slot[KMAX];
     float wj[KMAX], dot[KMAX];
 #pragma unroll
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(kCombineGradWaves * kWave) void combine_grad_kernel
       for (int j = 0; j < KMAX; ++j)
         if (slot[j] >= 0) v[j] = load_chunk(&y[(int64_t)slot[j] * d.chunks + c]);
       float g[8];
-      load_values<F32>(grad_out, (int64_t)t * d.chunks + c, g);
+      load_values<F32>(grad_out, t * d.chunks + c, g);
 #pragma unroll
       for (int j = 0; j < KMAX; ++j) {
         if (slot[j] < 0) continue;

@@ -392,8 +392,9 @@ def test_router(T, E, k, R, G, nodes, dtype, how, dev):
             ww = ref.router_weights(values, want, score, renorm, 2.5)
             # exp of x - max: its argument rounds once (|x - max| u in the result), exp and the
             # sums of up to E terms a few u; subnormal results flush by at most 2^-126
-            spread = np.minimum(np.nan_to_num(np.abs(values - values.max(1, keepdims=True)), nan=0.0,
-                                              posinf=0.0, neginf=0.0), 100).max()
+            with np.errstate(invalid="ignore"):
+                spread = np.abs(values - values.max(1, keepdims=True))
+            spread = np.minimum(np.nan_to_num(spread, nan=0.0, posinf=0.0, neginf=0.0), 100).max()
             rel = (16 + E + 4 * spread) * U
             check(w, ww, rel * ww + 2.5 * 2.0 ** -120, f"w {score} {renorm}")
             gl = plan.router_backward(xd, idx, gw.to(dev), score, renorm, 2.5)
@@ -535,6 +536,52 @@ def test_layer_in_a_graph_and_on_another_stream(dev):
             assert same(eager[j], outs[j]) == [], (i, j)
 
 
+def test_products_captured_on_their_own(dev):
+    # Small plans leave the offsets' scan to the first call that needs them.  One that is only
+    # recorded into a graph does not count for eager calls, and a graph replayed after another
+    # route of the plan uses that route.
+    rng = np.random.default_rng(2)
+    T, E, k, K, N = 90, 7, 2, 72, 136
+    idx, _, x, w, _, _ = expert_inputs(rng, T, E, k, K, N, "uniform", "none")
+    other = random_routing(rng, T, E, k, "skewed")
+    xd, wd = bf16(x, dev), bf16(w, dev)
+    routes = [torch.from_numpy(i).to(dev) for i in (idx, other)]
+    want = [cs.Plan(T, 8, E, k, 1).route(i).expert_linear(xd, wd)[0] for i in routes]
+    assert not torch.equal(*want)
+    plan = cs.Plan(T, 8, E, k, 1).route(routes[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, _ = plan.expert_linear(xd, wd)
+        again, _ = plan.expert_linear(xd, wd)
+    assert torch.equal(plan.expert_linear(xd, wd)[0], want[0])
+    for i in (0, 1, 0, 1):
+        plan.route(routes[i])
+        y.zero_()
+        again.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[i]) and torch.equal(again, want[i])
+        assert torch.equal(plan.expert_linear(xd, wd)[0], want[i])
+
+
+def test_outputs_and_workspace_given(dev):
+    m = Layer(40, 72, 64, 6, 2, 1, dev, seed=4)
+    s = m.step()
+    p = m.plan
+    args = (s["grad_h"], s["recv"], m.w1, s["pre"], "swiglu")
+    outs = [torch.empty_like(s[n]) for n in ("grad_recv", "grad_w1", "grad_b1")]
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=dev)
+    got = cs.expert_linear_backward(p, *args, bias_grad=True, grad_x=outs[0], grad_w=outs[1],
+                                    grad_bias=outs[2], workspace=ws)
+    for o, g, n in zip(outs, got, ("grad_recv", "grad_w1", "grad_b1")):
+        assert o.data_ptr() == g.data_ptr() and torch.equal(o, s[n])
+    with pytest.raises(ValueError, match="grad_w"):
+        cs.expert_linear_backward(p, *args, grad_w=outs[1].float())
+    with pytest.raises(cs.MoeError):      # a workspace that is not 256-byte aligned
+        cs.expert_linear_backward(p, *args, workspace=ws[16:])
+
+
 def test_given_stream_is_used(dev):
     # The calls run on the stream they are given, after what is queued there.
     m = Layer(64, 64, 64, 8, 2, 1, dev, seed=1)
@@ -594,3 +641,30 @@ def test_offsets_past_32_bits(dev):
     assert torch.equal(grad_y, recv)
     assert torch.equal(gwt, (x.float() ** 2).sum(1, keepdim=True).expand(T, k))
     assert slot.max() == T * k - 1
+
+
+@pytest.mark.slow
+def test_most_rows(dev):
+    # The most tokens that the 32-bit row indices allow, one expert and rows of 16 bytes: token t's
+    # row is row t.
+    T = 2 ** 31 - 4098
+    if torch.cuda.mem_get_info()[0] < 200 * (1 << 30):
+        pytest.skip("needs about 180 GiB of free device memory")
+    plan = cs.Plan(T, 8, 1, 1, 1)
+    plan.route(torch.zeros(T, 1, dtype=torch.int32, device=dev))
+    y = torch.empty(T, 8, dtype=torch.bfloat16, device=dev)
+    part = 1 << 26
+    for a in range(0, T, part):
+        b = min(T, a + part)
+        y[a:b] = ((torch.arange(a, b, device=dev)[:, None] * 8 + torch.arange(8, device=dev)) % 7 - 3)
+    g = torch.full((T, 8), 2.0, dtype=torch.bfloat16, device=dev)
+    g[T - 5:] = 1.0
+    w = torch.full((T, 1), 0.5, device=dev)
+    gx = plan.dispatch_backward(y)
+    for a in range(0, T, part):
+        assert torch.equal(gx[a: a + part], y[a: a + part]), a
+    gy, gw = plan.combine_backward(g, y, w, grad_y=gx)
+    for a in range(0, T, part):
+        s = slice(a, a + part)
+        assert torch.equal(gy[s], 0.5 * g[s]), a
+        assert torch.equal(gw[s], (g[s].float() * y[s].float()).sum(1, keepdim=True)), a
