@@ -4,31 +4,48 @@
 //   rows grad  gx = gz w[e]                                 contracts over Z
 //   wgrad      gw[e] = gz^T x                               contracts over e's rows
 //
-// One block computes one BM x BN tile of one expert's result with bf16 matrix
+// A block computes BM x BN tiles, one after another, with bf16 matrix
 // instructions (16x16x32) and float32 accumulators that stay in registers.
-// Per step of 64 along the contraction both operands' tiles are loaded
-// straight into LDS (buffer loads with an LDS destination), two stages deep:
-// the loads of the next step are in flight while this one is multiplied.
+// Per step of 32 along the contraction both operands' tiles are loaded
+// straight into LDS (buffer loads with an LDS destination), three stages deep,
+// and a step's fragments are read from LDS while the previous step's are
+// multiplied; the loads run on from one tile to the next.
+//
+// What bounds it.  Products of large square matrices run into the power
+// limit: 8192^3 takes 870 to 940 us in all three directions (1.17 to 1.27
+// PFLOP/s, matrix cores busy 65% of the cycles at 1.9 GHz; the library's
+// product of the same matrices 777 us, 87% at 1.6 GHz).  The experts' products
+// add to that the traffic of the weights and rows, which costs time even
+// under the multiplications: 64 experts, 4096 tokens, top-8, 2048 -> 2 x 1024
+// takes 335 to 375 us, where one matrix of the same 275 GFLOP takes 250 and
+// the 0.87 GB that it reads and writes 180 at the rate of a copy.  Steps:
+// fragments read a step ahead of their products and reads that do not wait
+// for loads under way (8192^3 from 1220, 1159 and 1447 us to 883, 870 and
+// 877), tiles grouped by XCD (half of that: from 50% of L2 requests missing),
+// three short stages instead of two long ones, 64-byte stores, and blocks
+// that go on from tile to tile (Zipf batch: 908 to 820 us).  Deeper
+// pipelines (four stages), smaller tiles, raised wave priority around the
+// products, streaming stores and heavy and light experts interleaved
+// measured equal or worse.
 //
 // An operand whose memory is contiguous along the contraction (x and w of
-// `rows`, gz of `rows grad`) is kept as rows of 64 values (128 bytes), one
-// 16-byte read per lane and fragment; an operand that is contiguous across it
-// (w of `rows grad`, both of wgrad) as 64 rows along the contraction, read
+// `rows`, gz of `rows grad`) is kept in LDS as rows of 32 values (64 bytes),
+// one 16-byte read per lane and fragment; an operand that is contiguous across
+// it (w of `rows grad`, both of wgrad) as 32 rows along the contraction, read
 // through the transposing LDS read.  Both layouts are swizzled so that the
-// lanes of a read fall into different banks; since a load to LDS writes lanes
-// one after another, the swizzle permutes which global chunk a lane loads.
+// lanes of a read fall into different banks (no conflict is counted); since a
+// load to LDS writes lanes one after another, the swizzle permutes which
+// global chunk a lane loads.
 //
-// Rows of different experts never share a tile, and the counts are only
-// known on the device: expert e's row tiles take the slots from
-// off[e] / BM + e on, which is at least ceil(rows / BM) slots each and
-// rows / BM + E in all; a block finds its expert by searching off and leaves
-// if its slot is not used.
+// Rows of different experts never share a tile.  The counts are only known
+// on the device: every block builds the list of the experts' row tiles in LDS
+// (about 2 us) and finds a tile's expert by searching it.
 //
 // Loads go through buffer descriptors that end with the operand's rows, so
 // rows past the end read as zeros; columns past the width of a transposed
 // operand give results that are not stored.  Chunks past the end of a
 // contiguous contraction are sent past the descriptor's end, so that they
-// read as zeros on both sides.
+// read as zeros on both sides (0 * NaN would not be 0).
 #include <algorithm>
 
 #include "layer_internal.h"
@@ -40,7 +57,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
 #define MOE_LDS __attribute__((address_space(3)))
 
 constexpr int kBK = 32;                   // contraction step: 64 bytes of bf16
@@ -247,9 +263,9 @@ __device__ __forceinline__ Segment segment_of(const RowTiles& t, const int32_t* 
   return s;
 }
 
-// The same for slots of BM rows that need no table: expert e's slots start at
-// off[e] / BM + e, which leaves at least ceil(rows / BM) slots each and makes
-// rows / BM + E in all; slots that no row falls into have rows <= 0.
+// The same for slots of bm rows that need no table: expert e's slots start at
+// off[e] / bm + e, which leaves at least ceil(rows / bm) slots each and makes
+// rows / bm + E in all; slots that no row falls into have rows <= 0.
 __device__ __forceinline__ Segment segment_of_slot(const int32_t* off, int E, int slot, int bm) {
   const int lane = threadIdx.x & (kWave - 1);
   const int step = (E + kWave - 1) / kWave;

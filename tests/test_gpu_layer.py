@@ -2,6 +2,8 @@
 element within the bound derived there, at the sizes, masks and routings where they can go wrong,
 and a whole layer forward and backward, eager and replayed from a captured graph."""
 
+import gc
+
 import numpy as np
 import pytest
 import torch
@@ -23,6 +25,14 @@ def dev():
     if not torch.cuda.is_available():
         pytest.skip("no GPU")
     return torch.device("cuda:0")
+
+
+@pytest.fixture
+def big_tensors():
+    """Gives the memory of a test of large tensors back, for the tests that follow."""
+    yield
+    gc.collect()
+    torch.cuda.empty_cache()
 
 
 def bf16(a, dev=None):
@@ -614,7 +624,7 @@ def test_timing_names_every_launch(dev):
 
 
 @pytest.mark.slow
-def test_offsets_past_32_bits(dev):
+def test_offsets_past_32_bits(dev, big_tensors):
     # Rows whose elements pass 2^31 (and byte offsets 2^32): the last rows against their values.
     T, k, E, H, N = 70000, 8, 16, 4096, 8
     rng = np.random.default_rng(0)
@@ -644,10 +654,11 @@ def test_offsets_past_32_bits(dev):
 
 
 @pytest.mark.slow
-def test_most_rows(dev):
+def test_most_rows(dev, big_tensors):
     # The most tokens that the 32-bit row indices allow, one expert and rows of 16 bytes: token t's
     # row is row t.
     T = 2 ** 31 - 4098
+    torch.cuda.empty_cache()
     if torch.cuda.mem_get_info()[0] < 200 * (1 << 30):
         pytest.skip("needs about 180 GiB of free device memory")
     plan = cs.Plan(T, 8, 1, 1, 1)
