@@ -88,7 +88,7 @@ LAYER_EXPORTS = (
     "moe_expert_linear", "moe_expert_backward_workspace_bytes", "moe_expert_linear_backward",
 )
 
-KERNEL_COUNT = 32  # moe_kernel and moe_layer_kernel
+KERNEL_COUNT = 33  # moe_kernel and moe_layer_kernel
 
 
 class MoeError(RuntimeError):

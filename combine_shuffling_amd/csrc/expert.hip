@@ -868,22 +868,22 @@ __global__ __launch_bounds__(kFewWaves * kWave) void expert_few_rows_kernel(
 
 // ---- rows grad: gx = gz w
 
+// Block `block` of `blocks`; lds: P::kLds + sizeof(RowTiles) bytes.
 template <typename P>
-__global__ __launch_bounds__(P::kThreads, 2) void expert_rows_grad_kernel(
-    ExpertDims x, const int32_t* __restrict__ off, const char* __restrict__ gz,
-    const char* __restrict__ w, uint16_t* __restrict__ gx, int ntiles) {
-  __shared__ __align__(1024) char lds[P::kLds + sizeof(RowTiles)];
+__device__ __forceinline__ void rows_grad(const ExpertDims& x, const int32_t* off, const char* gz,
+                                          const char* w, uint16_t* gx, int ntiles, char* lds,
+                                          int block, int blocks) {
   RowTiles& table = *reinterpret_cast<RowTiles*>(lds + P::kLds);
   table.build<P::BM, P::kThreads>(off, x.E);
   const TileGrid<P::BM, P::BN> grid(1, __builtin_amdgcn_readfirstlane(table.first[x.E]), ntiles);
   const int numbers = grid.numbers();
   const uint32_t lda = (uint32_t)x.Z * 2, ldb = (uint32_t)x.K * 2;
-  int number = blockIdx.x, n_ahead = 0;
+  int number = block, n_ahead = 0;
   Segment ahead{0, 0, 0};
   auto next = [&](typename P::Cursor& c) {
     c = {gz, w, 0, 0, 0, 0};
     ahead.rows = 0;
-    for (; number < numbers; number += gridDim.x) {
+    for (; number < numbers; number += blocks) {
       const Tile t = grid.at(number);
       if (!t.live) continue;
       const Segment s = ahead = segment_of<P::BM>(table, off, x.E, t.m);
@@ -893,7 +893,7 @@ __global__ __launch_bounds__(P::kThreads, 2) void expert_rows_grad_kernel(
       c.b = w + (int64_t)s.e * x.Z * ldb + t.n * P::BN * 2;
       c.b_bytes = (uint32_t)(t.n * P::BN * 2);
       c.len = x.Z;
-      number += gridDim.x;
+      number += blocks;
       break;
     }
   };
@@ -924,22 +924,23 @@ __global__ __launch_bounds__(P::kThreads, 2) void expert_rows_grad_kernel(
 
 // ---- wgrad: gw[e] = gz^T x
 
+// Block `block` of `blocks`; lds: P::kLds bytes.
 template <typename P, bool F32>
-__global__ __launch_bounds__(P::kThreads, 2) void expert_wgrad_kernel(
-    ExpertDims x, const int32_t* __restrict__ off, const char* __restrict__ gz,
-    const char* __restrict__ a, void* __restrict__ gw, TileGrid<P::BM, P::BN> grid) {
-  __shared__ __align__(1024) char lds[P::kLds];
+__device__ __forceinline__ void wgrad(const ExpertDims& x, const int32_t* off, const char* gz,
+                                      const char* a, void* gw,
+                                      const TileGrid<P::BM, P::BN>& grid, char* lds, int block,
+                                      int blocks) {
   const int numbers = grid.numbers();
   const uint32_t lda = (uint32_t)x.Z * 2, ldb = (uint32_t)x.K * 2;
   // A tile's bands follow each other.
-  int number = blockIdx.x, band = x.bands - 1;
+  int number = block, band = x.bands - 1;
   Tile ahead{0, 0, 0, false};
   auto next = [&](typename P::Cursor& c) {
     c = {gz, a, 0, 0, 0, 0};
-    if (++band < x.bands) number -= gridDim.x;
+    if (++band < x.bands) number -= blocks;
     band = band < x.bands ? band : 0;
     ahead.live = false;
-    for (; number < numbers; number += gridDim.x) {
+    for (; number < numbers; number += blocks) {
       const Tile t = grid.at(number);
       if (!t.live) continue;
       ahead = t;
@@ -950,7 +951,7 @@ __global__ __launch_bounds__(P::kThreads, 2) void expert_wgrad_kernel(
       c.b = a + o0 * ldb + t.n * P::BN * 2;
       c.b_bytes = (uint32_t)(t.n * P::BN * 2);
       c.len = x.rows > 0 ? o[1] - (int)o0 : 0;
-      number += gridDim.x;
+      number += blocks;
       break;
     }
   };
@@ -986,6 +987,40 @@ __global__ __launch_bounds__(P::kThreads, 2) void expert_wgrad_kernel(
       }
     }
   }
+}
+
+// ---- the kernels of the two gradients, apart and in one launch
+
+template <typename P>
+__global__ __launch_bounds__(P::kThreads, 2) void expert_rows_grad_kernel(
+    ExpertDims x, const int32_t* __restrict__ off, const char* __restrict__ gz,
+    const char* __restrict__ w, uint16_t* __restrict__ gx, int ntiles) {
+  __shared__ __align__(1024) char lds[P::kLds + sizeof(RowTiles)];
+  rows_grad<P>(x, off, gz, w, gx, ntiles, lds, blockIdx.x, gridDim.x);
+}
+
+template <typename P, bool F32>
+__global__ __launch_bounds__(P::kThreads, 2) void expert_wgrad_kernel(
+    ExpertDims x, const int32_t* __restrict__ off, const char* __restrict__ gz,
+    const char* __restrict__ a, void* __restrict__ gw, TileGrid<P::BM, P::BN> grid) {
+  __shared__ __align__(1024) char lds[P::kLds];
+  wgrad<P, F32>(x, off, gz, a, gw, grid, lds, blockIdx.x, gridDim.x);
+}
+
+// The first row_blocks blocks compute gx, the others gw.
+template <typename PR, typename PW, bool F32>
+__global__ __launch_bounds__(PR::kThreads, 2) void expert_grads_kernel(
+    ExpertDims x, const int32_t* __restrict__ off, const char* __restrict__ gz,
+    const char* __restrict__ w, uint16_t* __restrict__ gx, int ntiles,
+    const char* __restrict__ a, void* __restrict__ gw, TileGrid<PW::BM, PW::BN> grid,
+    int row_blocks) {
+  static_assert(PR::kThreads == PW::kThreads && PR::kLds >= PW::kLds);
+  __shared__ __align__(1024) char lds[PR::kLds + sizeof(RowTiles)];
+  if ((int)blockIdx.x < row_blocks)
+    rows_grad<PR>(x, off, gz, w, gx, ntiles, lds, blockIdx.x, row_blocks);
+  else
+    wgrad<PW, F32>(x, off, gz, a, gw, grid, lds, (int)blockIdx.x - row_blocks,
+                   (int)gridDim.x - row_blocks);
 }
 
 // ---- the activation's gradient, and the bias gradient
@@ -1127,6 +1162,14 @@ bool few_rows(const ExpertDims& x) {
   return x.rows <= most || (x.rows <= 2 * most && (int64_t)x.E * tiles <= kCus / 2);
 }
 
+// Large tiles for the weight gradient where every CU gets at least four of them
+// (64 experts, 4096 tokens, top-8, 2048 x 2048: 347 us against 365; 1021 tokens,
+// 1000 x 776, 480 tiles: 23.4 us against 22.6; one expert of 32768 rows, 64 tiles:
+// 745 against 497).
+bool large_weight_tiles(const ExpertDims& x) {
+  return (int64_t)x.E * ceil_div(x.Z, 256) * ceil_div(x.K, 256) >= 4 * kCus;
+}
+
 // Blocks for the row products: the most row tiles there can be are
 // rows / BM + E (the counts are only known on the device).
 template <typename P>
@@ -1157,7 +1200,8 @@ struct Type {
 
 template <int BM, int WM, bool GATED>
 using RowsTile = TileProduct<BM, 256, WM, 4, false, false, GATED>;
-using RowsGradTile = TileProduct<128, 256, 1, 4, false, true, false>;
+template <int BM, int WM>
+using RowsGradTile = TileProduct<BM, 256, WM, 4, false, true, false>;
 template <int BM, int WM>
 using WgradTile = TileProduct<BM, 256, WM, 4, true, true, false>;
 
@@ -1207,7 +1251,7 @@ hipError_t launch_expert_rows(const ExpertDims& x, const int32_t* off, const uin
 
 hipError_t launch_expert_rows_grad(const ExpertDims& x, const int32_t* off, const uint16_t* gz,
                                    const uint16_t* w, uint16_t* gx, hipStream_t s) {
-  using P = RowsGradTile;
+  using P = RowsGradTile<128, 1>;
   const int ntiles = ceil_div(x.K, P::BN);
   return by_band(x, off, [&](const ExpertDims& xb, const int32_t* ob, int) {
     return launch(MOE_KERNEL_EXPERT_ROWS_GRAD, expert_rows_grad_kernel<P>, row_blocks<P>(xb, ntiles),
@@ -1226,12 +1270,42 @@ hipError_t launch_expert_wgrad(const ExpertDims& x, const int32_t* off, const ui
                   dim3(std::min(grid.numbers(), blocks_at_once<P>())), dim3(P::kThreads), 0, s, x, off,
                   reinterpret_cast<const char*>(gz), reinterpret_cast<const char*>(a), gw, grid);
   };
-  // Large tiles where every CU gets at least four of them (64 experts, 4096
-  // tokens, top-8, 2048 x 2048: 347 us against 365; 1021 tokens, 1000 x 776, 480 tiles:
-  // 23.4 us against 22.6; one expert of 32768 rows, 64 tiles: 745 against 497).
-  const int64_t tiles = (int64_t)x.E * ceil_div(x.Z, 256) * ceil_div(x.K, 256);
-  if (tiles >= 4 * kCus) return go(Type<WgradTile<256, 2>>());
+  if (large_weight_tiles(x)) return go(Type<WgradTile<256, 2>>());
   return go(Type<WgradTile<128, 1>>());
+}
+
+// Both gradients in one launch, so that the few blocks that one of them has left
+// at its end run beside the other's.  Both in tiles of 256 rows where the weight
+// gradient takes those on its own, else both in tiles of 128 (a launch has one
+// size of block).  Apart and together, in us: 1021 tokens, 30 experts, top-4,
+// 776 -> 1000: 43.6, 36.5; 64 experts, top-8, 2048 -> 1024 gated, 256 tokens: 275,
+// 235; 1024: 343, 305; 2048: 426, 428; 4096: 672, 653; 8192 uneven tokens, 128
+// experts, 1024 -> 4096: 1490, 1391.  Tiles of 128 in the large launches: 256
+// tokens 225, 1024 tokens 333, 16384 tokens of 8 experts, 4096 x 4096, 2362 against
+// 1863.  A plan of several bands computes them apart: its weight gradient takes
+// all bands at once, the other goes band by band.
+hipError_t launch_expert_grads(const ExpertDims& x, const int32_t* off, const uint16_t* gz,
+                               const uint16_t* w, uint16_t* gx, const uint16_t* a, void* gw,
+                               bool f32, hipStream_t s) {
+  if (x.bands > 1) {
+    const hipError_t e = launch_expert_wgrad(x, off, gz, a, gw, f32, s);
+    return e != hipSuccess ? e : launch_expert_rows_grad(x, off, gz, w, gx, s);
+  }
+  auto go = [&](auto rows_tile, auto weight_tile) {
+    using PR = typename decltype(rows_tile)::type;
+    using PW = typename decltype(weight_tile)::type;
+    const int ntiles = ceil_div(x.K, PR::BN);
+    const TileGrid<PW::BM, PW::BN> grid(x.E, ceil_div(x.Z, PW::BM), ceil_div(x.K, PW::BN));
+    const int rb = (int)row_blocks<PR>(x, ntiles).x;
+    const int wb = std::min(grid.numbers(), blocks_at_once<PW>());
+    return launch(MOE_KERNEL_EXPERT_GRADS,
+                  f32 ? expert_grads_kernel<PR, PW, true> : expert_grads_kernel<PR, PW, false>,
+                  dim3(rb + wb), dim3(PR::kThreads), 0, s, x, off,
+                  reinterpret_cast<const char*>(gz), reinterpret_cast<const char*>(w), gx, ntiles,
+                  reinterpret_cast<const char*>(a), gw, grid, rb);
+  };
+  if (large_weight_tiles(x)) return go(Type<RowsGradTile<256, 2>>(), Type<WgradTile<256, 2>>());
+  return go(Type<RowsGradTile<128, 1>>(), Type<WgradTile<128, 1>>());
 }
 
 hipError_t launch_expert_act_grad(const ExpertDims& x, const int32_t* off, const uint16_t* gy,

@@ -271,8 +271,8 @@ const char* moe_kernel_name(int32_t kernel) {
       "combine_pn_kernel",
       "router_kernel",        "router_grad_kernel",     "dispatch_grad_kernel",
       "combine_grad_kernel",  "expert_rows_kernel",     "expert_few_rows_kernel",
-      "expert_rows_grad_kernel", "expert_wgrad_kernel", "expert_act_grad_kernel",
-      "expert_bias_sum_kernel"};
+      "expert_rows_grad_kernel", "expert_wgrad_kernel", "expert_grads_kernel",
+      "expert_act_grad_kernel", "expert_bias_sum_kernel"};
   return kernel >= 0 && kernel < MOE_LAYER_KERNEL_END ? names[kernel] : "?";
 }
 

@@ -617,7 +617,9 @@ def test_timing_names_every_launch(dev):
     for T in (4, 300):   # few rows an expert, and many
         m = Layer(T, 264, 136, 12, 4, 3, dev, seed=5)
         m.plan.timing(64)
-        m.step()
+        s = m.step()
+        for which in (dict(x_grad=False), dict(w_grad=False)):
+            m.plan.expert_linear_backward(s["grad_y"], s["h"], m.w2, **which)
         names |= {n for n, _, ms in m.plan.timing_read() if ms > 0}
         m.plan.timing(0)
     assert {_abi.kernel_name(i) for i in range(22, _abi.KERNEL_COUNT)} <= names

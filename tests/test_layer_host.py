@@ -119,17 +119,17 @@ def test_expert_config_refusals(cfg, want):
 
 
 def test_backward_workspace_bytes():
-    # grad_z (with an activation) and 64-row partial sums of every column
+    # grad_z (with an activation) and 32-row partial sums of every column
     p = plan(T=100, E=8, k=2)
     L = _abi.lib()
     size = lambda *c: L.moe_expert_backward_workspace_bytes(p._h, ctypes.byref(_abi.ExpertConfig(*c)))  # noqa: E731
-    slots = 200 // 64 + 8
+    slots = 200 // 32 + 8
     assert size(64, 64, 0) == slots * 64 * 4
     assert size(64, 64, 4) == 200 * 128 * 2 + slots * 128 * 4
     assert size(64, 40, 2) % 256 == 0
     # banded: every band has slots of its own for its experts
     p = plan(T=1024, band_tokens=256)
-    assert size(64, 64, 0) == (2048 // 64 + 4 * 8) * 64 * 4
+    assert size(64, 64, 0) == (2048 // 32 + 4 * 8) * 64 * 4
     assert L.moe_expert_linear(p._h, None, vp(16), vp(16), None, None, vp(16), None, None) == BAD
 
 
@@ -138,7 +138,8 @@ def test_kernel_names():
     assert names == ["router_kernel", "router_grad_kernel", "dispatch_grad_kernel",
                      "combine_grad_kernel", "expert_rows_kernel", "expert_few_rows_kernel",
                      "expert_rows_grad_kernel",
-                     "expert_wgrad_kernel", "expert_act_grad_kernel", "expert_bias_sum_kernel"]
+                     "expert_wgrad_kernel", "expert_grads_kernel",
+                     "expert_act_grad_kernel", "expert_bias_sum_kernel"]
 
 
 # ---- the Python binding's own checks
