@@ -363,6 +363,13 @@ ROUTER = [
     (9, 1024, 16, 4, 4, 0),
     (40, 300, 16, 3, 3, 0),
     (300, 16, 16, 1, 1, 0),      # every expert
+    # tokens that share a wave
+    (4099, 64, 8, 8, 8, 0),
+    (4097, 100, 6, 10, 2, 3),
+    (5003, 30, 16, 30, 2, 8),    # 15 nodes of 2
+    (4101, 256, 8, 64, 8, 4),
+    (4100, 130, 5, 18, 3, 2),    # nodes of 24, 22, 21, 21, 21 and 21
+    (4098, 200, 4, 20, 1, 2),    # more nodes than lanes: a wave each
 ]
 
 
@@ -377,22 +384,24 @@ def nodes_of_experts(E, R, G):
 def test_router(T, E, k, R, G, nodes, dtype, how, dev):
     say(f"[layer] router T={T} E={E} k={k} nodes={nodes} {dtype} {how}")
     rng = np.random.default_rng(T + E)
-    x = torch.from_numpy(rng.normal(size=(T, E)).astype(np.float32) * 2)
+    rows = np.arange(T) % 301   # large batches repeat rows, so that the definition has few to do
+    x = torch.from_numpy(rng.normal(size=(min(T, 301), E)).astype(np.float32) * 2)
     if how == "masked":       # rows that a mask leaves nothing of, or less than k; NaN; infinity
-        x[rng.random((T, E)) < 0.6] = -np.inf
+        x[rng.random(x.shape) < 0.6] = -np.inf
         x[0] = -np.inf
         if T > 4:
             x[1], x[2, E // 2], x[3, ::2], x[4, E - 1] = float("nan"), float("nan"), np.inf, np.inf
             x[2, E // 3] = torch.finfo(torch.bfloat16).min
     if how == "huge":         # far from 0, where exp over- and underflows
         x = x * 40 - 60
-    x = x.to(dtype)
+    few = x.to(dtype)
+    x = few[rows]
     bias = rng.normal(size=E).astype(np.float32) if how == "bias" else None
     plan = cs.Plan(T, 8, E, k, R, G)
     xd = x.to(dev)
     values = x.double().numpy()
     node_of = nodes_of_experts(E, R, G)
-    want = ref.router_choice(x.float().numpy(), bias, k, node_of, nodes)
+    want = ref.router_choice(few.float().numpy(), bias, k, node_of, nodes)[rows]
     gw = torch.from_numpy(rng.normal(size=(T, k)).astype(np.float32))
     for score in ("softmax", "sigmoid"):
         for renorm in (True, False):
