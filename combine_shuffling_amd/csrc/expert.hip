@@ -991,6 +991,42 @@ __device__ __forceinline__ void wgrad(const ExpertDims& x, const int32_t* off, c
   }
 }
 
+// grad_bias: the partial sums of an expert's slots, one column a thread (block
+// `block` of THREADS columns), eight loads at a time.
+template <int THREADS>
+__device__ __forceinline__ void bias_sum(const ExpertDims& x, const int32_t* __restrict__ off,
+                                         const float* __restrict__ partial, float* __restrict__ gb,
+                                         int block) {
+  const int strips = (x.Z + THREADS - 1) / THREADS;
+  const int e = block / strips, n = block % strips * THREADS + threadIdx.x;
+  if (n >= x.Z) return;
+  float t = 0.0f;
+  for (int b = 0; b < (x.rows > 0 ? x.bands : 0); ++b) {
+    const int o0 = off[b * (x.E + 1) + e], rows = off[b * (x.E + 1) + e + 1] - o0;
+    const int used = (rows + kBiasRows - 1) / kBiasRows;
+    const float* p = partial + (o0 / kBiasRows + e + (int64_t)b * x.E) * x.Z + n;
+    int i = 0;
+    for (; i + 8 <= used; i += 8, p += (int64_t)8 * x.Z) {  // eight loads at a time, added in order
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = p[(int64_t)q * x.Z];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) t += v[q];
+    }
+    for (; i < used; ++i, p += x.Z) t += *p;
+  }
+  gb[(int64_t)e * x.Z + n] = t;
+}
+
+// Bound by the longest chain of loads: 30 experts of 136 rows 4.0 us, which any launch
+// takes; one expert of 8192 rows among 64 (256 slots) 19.6.
+constexpr int kBiasThreads = 256;
+__global__ __launch_bounds__(kBiasThreads) void expert_bias_sum_kernel(
+    ExpertDims x, const int32_t* __restrict__ off, const float* __restrict__ partial,
+    float* __restrict__ gb) {
+  bias_sum<kBiasThreads>(x, off, partial, gb, blockIdx.x);
+}
+
 // ---- the kernels of the two gradients, apart and in one launch
 
 template <typename P>
@@ -1009,20 +1045,23 @@ __global__ __launch_bounds__(P::kThreads, 2) void expert_wgrad_kernel(
   wgrad<P, F32>(x, off, gz, a, gw, grid, lds, blockIdx.x, gridDim.x);
 }
 
-// The first row_blocks blocks compute gx, the others gw.
+// The first bias_blocks blocks compute gb, the next row_blocks gx, the others gw.
 template <typename PR, typename PW, bool F32>
 __global__ __launch_bounds__(PR::kThreads, 2) void expert_grads_kernel(
     ExpertDims x, const int32_t* __restrict__ off, const char* __restrict__ gz,
     const char* __restrict__ w, uint16_t* __restrict__ gx, int ntiles,
     const char* __restrict__ a, void* __restrict__ gw, TileGrid<PW::BM, PW::BN> grid,
-    int row_blocks) {
+    const float* __restrict__ partial, float* __restrict__ gb, int row_blocks, int bias_blocks) {
   static_assert(PR::kThreads == PW::kThreads && PR::kLds >= PW::kLds);
   __shared__ __align__(1024) char lds[PR::kLds + sizeof(RowTiles)];
-  if ((int)blockIdx.x < row_blocks)
-    rows_grad<PR>(x, off, gz, w, gx, ntiles, lds, blockIdx.x, row_blocks);
+  const int block = (int)blockIdx.x - bias_blocks;
+  if (block < 0)
+    bias_sum<PR::kThreads>(x, off, partial, gb, blockIdx.x);
+  else if (block < row_blocks)
+    rows_grad<PR>(x, off, gz, w, gx, ntiles, lds, block, row_blocks);
   else
-    wgrad<PW, F32>(x, off, gz, a, gw, grid, lds, (int)blockIdx.x - row_blocks,
-                   (int)gridDim.x - row_blocks);
+    wgrad<PW, F32>(x, off, gz, a, gw, grid, lds, block - row_blocks,
+                   (int)gridDim.x - bias_blocks - row_blocks);
 }
 
 // ---- the activation's gradient, and the bias gradient
@@ -1112,34 +1151,6 @@ __global__ __launch_bounds__(kActCols * kActRows) void expert_act_grad_kernel(
     if (col0 + n < x.N)
       partial[((int64_t)slot + (int64_t)band * x.E) * x.Z + h * x.N + col0 + n] = t;
   }
-}
-
-// grad_bias: the partial sums of an expert's slots, one column a thread, eight
-// loads at a time.  Bound by the longest chain of them: 30 experts of 136 rows 4.0
-// us, which any launch takes; one expert of 8192 rows among 64 (256 slots) 19.6.
-__global__ __launch_bounds__(256) void expert_bias_sum_kernel(ExpertDims x,
-                                                              const int32_t* __restrict__ off,
-                                                              const float* __restrict__ partial,
-                                                              float* __restrict__ gb) {
-  const int strips = (x.Z + 255) / 256;
-  const int e = blockIdx.x / strips, n = blockIdx.x % strips * 256 + threadIdx.x;
-  if (n >= x.Z) return;
-  float t = 0.0f;
-  for (int b = 0; b < (x.rows > 0 ? x.bands : 0); ++b) {
-    const int o0 = off[b * (x.E + 1) + e], rows = off[b * (x.E + 1) + e + 1] - o0;
-    const int used = (rows + kBiasRows - 1) / kBiasRows;
-    const float* p = partial + (o0 / kBiasRows + e + (int64_t)b * x.E) * x.Z + n;
-    int i = 0;
-    for (; i + 8 <= used; i += 8, p += (int64_t)8 * x.Z) {  // eight loads at a time, added in order
-      float v[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = p[(int64_t)q * x.Z];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) t += v[q];
-    }
-    for (; i < used; ++i, p += x.Z) t += *p;
-  }
-  gb[(int64_t)e * x.Z + n] = t;
 }
 
 // Launches `total` blocks in ranges of at most kMaxTileBlocks.
@@ -1290,10 +1301,19 @@ hipError_t launch_expert_wgrad(const ExpertDims& x, const int32_t* off, const ui
 // experts, 1024 -> 4096: 1490, 1391.  Tiles of 128 in the large launches: 256
 // tokens 225, 1024 tokens 333, 16384 tokens of 8 experts, 4096 x 4096, 2362 against
 // 1863.  A plan of several bands computes them apart: its weight gradient takes
-// all bands at once, the other goes band by band.
+// all bands at once, the other goes band by band.  The bias sums join them where
+// they are a block a CU at most, ahead of the tiles' blocks, which are fewer on a
+// CU than theirs would be in a launch of their own.
 hipError_t launch_expert_grads(const ExpertDims& x, const int32_t* off, const uint16_t* gz,
                                const uint16_t* w, uint16_t* gx, const uint16_t* a, void* gw,
-                               bool f32, hipStream_t s) {
+                               bool f32, const float* partial, float* gb, hipStream_t s) {
+  const int threads = large_weight_tiles(x) ? WgradTile<256, 2>::kThreads : WgradTile<128, 1>::kThreads;
+  int64_t bias_blocks = gb != nullptr ? (int64_t)x.E * ceil_div(x.Z, threads) : 0;
+  if (x.bands > 1 || bias_blocks > kCus) {
+    const hipError_t e = gb != nullptr ? launch_expert_bias_sum(x, off, partial, gb, s) : hipSuccess;
+    if (e != hipSuccess) return e;
+    bias_blocks = 0;
+  }
   if (x.bands > 1) {
     const hipError_t e = launch_expert_wgrad(x, off, gz, a, gw, f32, s);
     return e != hipSuccess ? e : launch_expert_rows_grad(x, off, gz, w, gx, s);
@@ -1307,9 +1327,9 @@ hipError_t launch_expert_grads(const ExpertDims& x, const int32_t* off, const ui
     const int wb = std::min(grid.numbers(), blocks_at_once<PW>());
     return launch(MOE_KERNEL_EXPERT_GRADS,
                   f32 ? expert_grads_kernel<PR, PW, true> : expert_grads_kernel<PR, PW, false>,
-                  dim3(rb + wb), dim3(PR::kThreads), 0, s, x, off,
+                  dim3((int)bias_blocks + rb + wb), dim3(PR::kThreads), 0, s, x, off,
                   reinterpret_cast<const char*>(gz), reinterpret_cast<const char*>(w), gx, ntiles,
-                  reinterpret_cast<const char*>(a), gw, grid, rb);
+                  reinterpret_cast<const char*>(a), gw, grid, partial, gb, rb, (int)bias_blocks);
   };
   if (large_weight_tiles(x)) return go(Type<RowsGradTile<256, 2>>(), Type<WgradTile<256, 2>>());
   return go(Type<RowsGradTile<128, 1>>(), Type<WgradTile<128, 1>>());
@@ -1333,7 +1353,8 @@ hipError_t launch_expert_act_grad(const ExpertDims& x, const int32_t* off, const
 hipError_t launch_expert_bias_sum(const ExpertDims& x, const int32_t* off, const float* partial,
                                   float* gb, hipStream_t s) {
   return launch(MOE_KERNEL_EXPERT_BIAS_SUM, expert_bias_sum_kernel,
-                dim3((uint32_t)(x.E * ceil_div(x.Z, 256))), dim3(256), 0, s, x, off, partial, gb);
+                dim3((uint32_t)(x.E * ceil_div(x.Z, kBiasThreads))), dim3(kBiasThreads), 0, s, x, off,
+                partial, gb);
 }
 
 }  // namespace moe

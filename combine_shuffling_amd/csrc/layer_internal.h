@@ -56,10 +56,11 @@ hipError_t launch_expert_rows_grad(const ExpertDims& x, const int32_t* off, cons
                                    const uint16_t* w, uint16_t* gx, hipStream_t s);
 hipError_t launch_expert_wgrad(const ExpertDims& x, const int32_t* off, const uint16_t* gz,
                                const uint16_t* a, void* gw, bool f32, hipStream_t s);
-// Both, in one launch on a plan of one band.
+// Both, in one launch on a plan of one band, and the bias gradient from its
+// partial sums (gb null: not wanted).
 hipError_t launch_expert_grads(const ExpertDims& x, const int32_t* off, const uint16_t* gz,
                                const uint16_t* w, uint16_t* gx, const uint16_t* a, void* gw,
-                               bool f32, hipStream_t s);
+                               bool f32, const float* partial, float* gb, hipStream_t s);
 // gz (bf16, null: not wanted) and partial (float32 [bias_slots, Z], null: not wanted).
 hipError_t launch_expert_act_grad(const ExpertDims& x, const int32_t* off, const uint16_t* gy,
                                   const uint16_t* pre, uint16_t* gz, float* partial,

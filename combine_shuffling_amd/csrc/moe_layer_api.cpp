@@ -186,13 +186,14 @@ moe_status moe_expert_linear_backward(moe_plan* plan, const moe_expert_config* c
     e = moe::launch_expert_act_grad(dims, off, grad_y, pre, act && products ? gz : nullptr,
                                     grad_bias ? partial : nullptr, s);
   const uint16_t* g = act ? gz : grad_y;
-  if (e == hipSuccess && grad_bias) e = moe::launch_expert_bias_sum(dims, off, partial, grad_bias, s);
   const bool f32 = w_dtype == MOE_OUT_F32;
   if (e == hipSuccess && grad_w && grad_x && !empty)
-    e = moe::launch_expert_grads(dims, off, g, w, grad_x, x, grad_w, f32, s);
-  else if (e == hipSuccess && grad_w)
+    return moe::from_hip(moe::launch_expert_grads(dims, off, g, w, grad_x, x, grad_w, f32, partial,
+                                                  grad_bias, s));
+  if (e == hipSuccess && grad_bias) e = moe::launch_expert_bias_sum(dims, off, partial, grad_bias, s);
+  if (e == hipSuccess && grad_w)
     e = moe::launch_expert_wgrad(dims, off, g, x, grad_w, f32, s);
-  else if (e == hipSuccess && grad_x && !empty)
+  if (e == hipSuccess && grad_x && !empty)
     e = moe::launch_expert_rows_grad(dims, off, g, w, grad_x, s);
   return moe::from_hip(e);
 }

@@ -165,7 +165,7 @@ typedef enum moe_layer_kernel {
   MOE_KERNEL_EXPERT_FEW_ROWS,  /* the same for batches of few rows an expert             */
   MOE_KERNEL_EXPERT_ROWS_GRAD, /* product of grad_z with expert weights: grad_x          */
   MOE_KERNEL_EXPERT_WGRAD,     /* product over an expert's rows: grad_w                  */
-  MOE_KERNEL_EXPERT_GRADS,     /* both of them, where both are wanted                   */
+  MOE_KERNEL_EXPERT_GRADS,     /* both of them, and few bias sums, where both are wanted */
   MOE_KERNEL_EXPERT_ACT_GRAD,  /* grad_z, and partial sums of the bias gradient          */
   MOE_KERNEL_EXPERT_BIAS_SUM,  /* the partial sums added up                              */
   MOE_LAYER_KERNEL_END

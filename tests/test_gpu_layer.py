@@ -627,7 +627,7 @@ def test_timing_names_every_launch(dev):
         m = Layer(T, 264, 136, 12, 4, 3, dev, seed=5)
         m.plan.timing(64)
         s = m.step()
-        for which in (dict(x_grad=False), dict(w_grad=False)):
+        for which in (dict(x_grad=False, bias_grad=True), dict(w_grad=False)):
             m.plan.expert_linear_backward(s["grad_y"], s["h"], m.w2, **which)
         names |= {n for n, _, ms in m.plan.timing_read() if ms > 0}
         m.plan.timing(0)
