@@ -30,6 +30,8 @@ the layer's gradients:
     grad_recv, grad_w1, _ = expert_linear_backward(plan, grad_h, recv, w1, pre, "swiglu")
     grad_x = dispatch_backward(plan, grad_recv)
     grad_logits = router_backward(plan, logits, idx, grad_w)
+
+Outputs may be given to these calls; they share no memory with other arguments.
 """
 
 from __future__ import annotations
@@ -100,17 +102,32 @@ def _out(t: torch.Tensor | None, shape, dtype, name: str, device) -> torch.Tenso
     return t
 
 
+def _apart(given, others) -> None:
+    """The outputs that the caller gives share no memory with each other or with an input."""
+    for i, t in enumerate(given):
+        if t is None:
+            continue
+        end = t.data_ptr() + t.numel() * t.element_size()
+        for o in (*given[i + 1:], *others):
+            if (o is not None and o.data_ptr() < end and
+                    t.data_ptr() < o.data_ptr() + o.numel() * o.element_size()):
+                raise ValueError("an output shares memory with another argument")
+
+
 def _addr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
 def _on_stream(method):
     """A call that also takes stream=: it then runs with that stream current, so that what it
-    allocates belongs to that stream too."""
+    allocates belongs to that stream too.  The stream has to be one of the tensors' device."""
     @functools.wraps(method)
     def call(*args, stream=None, **kw):
         if stream is None:
             return method(*args, **kw)
+        for t in (*args, *kw.values()):
+            if isinstance(t, torch.Tensor) and t.device != stream.device:
+                raise ValueError(f"stream is on {stream.device}, a tensor on {t.device}")
         with torch.cuda.stream(stream):
             return method(*args, **kw)
     return call
@@ -366,6 +383,8 @@ class Plan:
         if bias is not None:
             _need(bias, (self.E,), _F32, "bias", dev)
         cfg = self._router_config(score, renormalise, nodes_per_token, scale)
+        if topk_idx is not None or topk_w is not None:
+            _apart((topk_idx, topk_w), (logits, bias))
         topk_idx = _out(topk_idx, (self.T, self.k), torch.int32, "topk_idx", dev)
         topk_w = _out(topk_w, (self.T, self.k), torch.float32, "topk_w", dev)
         self._launch("moe_router", dev, cfg, logits.data_ptr(), _OUT_CODE[logits.dtype],
@@ -384,6 +403,8 @@ class Plan:
         _need(topk_idx, (self.T, self.k), (torch.int32,), "topk_idx", dev)
         _need(grad_w, (self.T, self.k), _F32, "grad_w", dev)
         cfg = self._router_config(score, renormalise, 0, scale)
+        if grad_logits is not None:
+            _apart((grad_logits,), (logits, topk_idx, grad_w))
         grad_logits = _out(grad_logits, (self.T, self.E), logits.dtype, "grad_logits", dev)
         self._launch("moe_router_backward", dev, cfg, logits.data_ptr(),
                      _OUT_CODE[logits.dtype], topk_idx.data_ptr(), grad_w.data_ptr(),
@@ -400,6 +421,8 @@ class Plan:
             raise MoeError(_abi.ERR_PLAN_NOT_ROUTED, "dispatch_backward")
         _need(grad_recv, (self.recv_rows, self.H), _BF16_LIKE, "grad_recv", dev)
         code = _out_code(out_dtype, "out_dtype")
+        if grad_x is not None:
+            _apart((grad_x,), (grad_recv,))
         grad_x = _out(grad_x, (self.T, self.H), out_dtype, "grad_x", dev)
         self._launch("moe_dispatch_backward", dev, grad_recv.data_ptr(), grad_x.data_ptr(),
                      code)
@@ -417,6 +440,8 @@ class Plan:
         _need(grad_out, (self.T, self.H), (torch.float32, torch.bfloat16), "grad_out", dev)
         _need(y, (self.recv_rows, self.H), _BF16_LIKE, "y", dev)
         _need(topk_w, (self.T, self.k), _F32, "topk_w", dev)
+        if grad_y is not None or grad_w is not None:
+            _apart((grad_y, grad_w), (grad_out, y, topk_w))
         grad_y = _out(grad_y, (self.recv_rows, self.H), torch.bfloat16, "grad_y", dev)
         grad_w = _out(grad_w, (self.T, self.k), torch.float32, "grad_w", dev)
         self._launch("moe_combine_backward", dev, grad_out.data_ptr(),
@@ -452,7 +477,8 @@ class Plan:
         y[r] = act(x[r] . w[e]^T + bias[e]) + residual[r] for each receive row r of expert e;
         x [T*k, K], w [E, Z, K], residual and y [T*k, N] bf16, bias [E, Z] float32; Z = 2N (gate
         rows, then up rows) with "swiglu" and "geglu", else N.  pre: the product before the
-        activation, [T*k, Z] bf16, with save_pre (or a tensor to write), else None."""
+        activation, [T*k, Z] bf16, with save_pre (or a tensor to write), else None.  K and N are
+        multiples of 8."""
         dev = self.device
         if dev is None:
             raise MoeError(_abi.ERR_PLAN_NOT_ROUTED, "expert_linear")
@@ -463,6 +489,8 @@ class Plan:
             _need(bias, (self.E, Z), _F32, "bias", dev)
         if residual is not None:
             _need(residual, (rows, N), _BF16, "residual", dev)
+        if y is not None or pre is not None:
+            _apart((y, pre), (x, w, bias, residual))
         y = _out(y, (rows, N), torch.bfloat16, "y", dev)
         if save_pre or pre is not None:
             pre = _out(pre, (rows, Z), torch.bfloat16, "pre", dev)
@@ -501,10 +529,18 @@ class Plan:
             pre = None
         code = _out_code(grad_w_dtype, "grad_w_dtype")
         need = self._lib.moe_expert_backward_workspace_bytes(self._h, cfg)
-        if workspace is not None and workspace.numel() * workspace.element_size() < need:
-            raise ValueError("workspace too small")
         if workspace is None:
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        else:
+            _need(workspace, getattr(workspace, "shape", ()), (getattr(workspace, "dtype", None),),
+                  "workspace", dev)
+            if workspace.numel() * workspace.element_size() < need:
+                raise ValueError("workspace too small")
+            _apart((workspace,), (grad_y, x, w, pre))
+        given = tuple(t for t, wanted in ((grad_x, x_grad), (grad_w, w_grad), (grad_bias, bias_grad))
+                      if wanted and t is not None)
+        if given:
+            _apart(given, (grad_y, x, w, pre, workspace))
         grad_x = _out(grad_x, (rows, K), torch.bfloat16, "grad_x", dev) if x_grad else None
         grad_w = _out(grad_w, (self.E, Z, K), grad_w_dtype, "grad_w", dev) if w_grad else None
         grad_bias = _out(grad_bias, (self.E, Z), torch.float32, "grad_bias", dev) if bias_grad else None

@@ -132,8 +132,9 @@ moe_status moe_expert_linear(moe_plan* plan, const moe_expert_config* cfg, const
                              uint16_t* y, uint16_t* pre, void* stream);
 
 /* Device workspace of moe_expert_linear_backward (bytes, a multiple of 256; 0
- * for a cfg that the call refuses): the gradient of z in bf16 with an activation, and the partial sums of
- * the bias gradient.  Its contents need no initialisation. */
+ * for a cfg that the call refuses): the gradient of z in bf16 with an
+ * activation, and the partial sums of the bias gradient.  Its contents need no
+ * initialisation. */
 size_t moe_expert_backward_workspace_bytes(const moe_plan* plan, const moe_expert_config* cfg);
 
 /* Gradient of moe_expert_linear, with grad_z = grad_y * act'(pre) (gated:

@@ -200,3 +200,56 @@ def test_binding_checks_expert_arguments():
             call()
     with pytest.raises(TypeError):
         p.expert_linear(x, None)
+
+
+def test_binding_refuses_outputs_that_share_memory():
+    p = plan()
+    p.device = torch.device("cpu")   # as if routed
+    bf = dict(dtype=torch.bfloat16)
+    logits, x, w = torch.zeros(64, 8), torch.zeros(128, 64, **bf), torch.zeros(8, 64, 64, **bf)
+    pre, go, k32 = torch.zeros(128, 64, **bf), torch.zeros(64, 64, **bf), torch.zeros(64, 2)
+    both = torch.zeros(128, 64, **bf)
+    for call in (lambda: p.router(logits, topk_w=logits.view(-1)[:128].view(64, 2)),
+                 lambda: p.router(logits, topk_idx=k32.view(torch.int32), topk_w=k32),
+                 lambda: p.router_backward(logits, k32.int(), k32, grad_logits=logits),
+                 lambda: p.dispatch_backward(x, grad_x=x[:64]),
+                 lambda: p.combine_backward(go, x, k32, grad_y=x),
+                 lambda: p.combine_backward(go, x, k32, grad_w=k32),
+                 lambda: p.expert_linear(x, w, residual=pre, y=pre),
+                 lambda: p.expert_linear(x, w, y=both, pre=both),
+                 lambda: p.expert_linear(x, w, y=x),
+                 lambda: p.expert_linear_backward(pre, x, w, grad_x=x),
+                 lambda: p.expert_linear_backward(pre, x, w, grad_w=w),
+                 lambda: p.expert_linear_backward(both, x, w, workspace=both.view(torch.uint8))):
+        with pytest.raises(ValueError, match="shares memory"):
+            call()
+    # neighbours in one buffer are apart
+    with pytest.raises(ValueError, match="GPU"):
+        p.dispatch_backward(x, grad_x=torch.zeros(192, 64, **bf)[128:])
+    buffer = torch.zeros(192, 64, **bf)
+    with pytest.raises(ValueError, match="GPU"):
+        p.dispatch_backward(buffer[:128], grad_x=buffer[128:])
+
+
+def test_binding_checks_the_workspace():
+    p = plan()
+    p.device = torch.device("cpu")
+    bf = dict(dtype=torch.bfloat16)
+    x, w, gy = torch.zeros(128, 64, **bf), torch.zeros(8, 32, 64, **bf), torch.zeros(128, 32, **bf)
+    with pytest.raises(ValueError, match="contiguous"):   # many elements, one byte of memory
+        p.expert_linear_backward(gy, x, w, workspace=torch.zeros(1, dtype=torch.uint8).expand(1 << 20))
+    with pytest.raises(ValueError, match="is on"):
+        p.expert_linear_backward(gy, x, w, workspace=torch.empty(1 << 20, device="meta"))
+    with pytest.raises(TypeError):
+        p.expert_linear_backward(gy, x, w, workspace=4096)
+
+
+def test_binding_refuses_a_stream_of_another_device():
+    class Elsewhere:
+        device = torch.device("cuda", 1)
+    p = plan()
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        p.router(torch.zeros(64, 8), stream=Elsewhere())
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        cs.router_backward(p, torch.zeros(64, 8), torch.zeros(64, 2, dtype=torch.int32),
+                           torch.zeros(64, 2), stream=Elsewhere())
