@@ -96,8 +96,9 @@ def _out_code(dtype, name: str) -> int:
 
 def _out(t: torch.Tensor | None, shape, dtype, name: str, device) -> torch.Tensor:
     """The caller's output tensor, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+    if t is None:   # torch.empty takes 0.4 us more, a twentieth of a small call
+        stride = (shape[1], 1) if len(shape) == 2 else (shape[1] * shape[2], shape[2], 1)
+        return torch.empty_strided(shape, stride, dtype=dtype, device=device)
     _need(t, shape, (dtype,), name, device)
     return t
 
@@ -178,7 +179,7 @@ class Plan:
         # The raw handle: making a torch.cuda.Stream object takes 2 us, a sixth of a small call.
         stream = torch._C._cuda_getCurrentRawStream(device.index)
         fn = getattr(self._lib, name)
-        if device.index == torch.cuda.current_device():
+        if device.index == torch._C._cuda_getDevice():
             st = fn(self._h, *args, stream)
         else:
             with torch.cuda.device(device):
