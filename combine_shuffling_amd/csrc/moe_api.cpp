@@ -109,25 +109,64 @@ Work bind_work(const Layout& l, void* base) {
   return w;
 }
 
-moe_status ensure_scanned(moe_plan* plan, hipStream_t s) {
-  if (plan->scanned && !plan->d.fused_scan && plan->scan_capture == 0) return MOE_OK;
-  hipStreamCaptureStatus capturing = hipStreamCaptureStatusNone;
-  unsigned long long id = 0;
-  if (hipStreamGetCaptureInfo(s, &capturing, &id) != hipSuccess) return MOE_ERR_HIP;
-  if (capturing != hipStreamCaptureStatusActive) id = 0;
-  if (plan->scanned && (plan->scan_capture == id || (plan->scan_capture == 0 && !plan->d.fused_scan)))
-    return MOE_OK;
-  if (launch_route_scan(plan->d, plan->work, s) != hipSuccess) return MOE_ERR_HIP;
-  plan->scanned = true;
-  plan->scan_capture = id;
+moe_status capture_of(hipStream_t s, CaptureId* id) {
+  *id = 0;
+  if (s == nullptr) return MOE_OK;  // the null stream is never captured
+  hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+  CaptureId v = 0;
+  if (hipStreamGetCaptureInfo(s, &status, &v) != hipSuccess) return MOE_ERR_HIP;
+  if (status == hipStreamCaptureStatusActive) *id = v;
   return MOE_OK;
 }
 
+namespace {
+
+// Whether a scan or an assign holds for a call in capture `now`: it was done
+// in the same capture, or outside of any on a plan routed outside of any.
+bool holds(const moe_plan* plan, bool done, CaptureId in, CaptureId now) {
+  if (plan->finished && (now == 0 || now == plan->route_capture)) return true;
+  return done && in == now && (now != 0 || plan->route_capture == 0);
+}
+
+moe_status scan_in(moe_plan* plan, CaptureId now, hipStream_t s) {
+  // the scan of larger plans is a part of every route
+  if (plan->scanned && !plan->d.fused_scan) return MOE_OK;
+  if (holds(plan, plan->scanned, plan->scan_capture, now)) return MOE_OK;
+  if (launch_route_scan(plan->d, plan->work, s) != hipSuccess) return MOE_ERR_HIP;
+  plan->scanned = true;
+  plan->scan_capture = now;
+  return MOE_OK;
+}
+
+// Binds a routing to the plan, in capture `now`.
+void bind_routing(moe_plan* plan, const int32_t* topk_idx, void* workspace, CaptureId now) {
+  plan->routed = plan->finished = plan->scanned = plan->assigned = false;
+  plan->route_capture = now;
+  plan->idx = topk_idx;
+  plan->ws = workspace;
+  plan->work = bind_work(plan->layout, workspace);
+}
+
+}  // namespace
+
+moe_status ensure_scanned(moe_plan* plan, hipStream_t s) {
+  CaptureId now;
+  const moe_status st = capture_of(s, &now);
+  return st != MOE_OK ? st : scan_in(plan, now, s);
+}
+
 moe_status ensure_assigned(moe_plan* plan, hipStream_t s) {
-  if (plan->assigned) return MOE_OK;
-  if (ensure_scanned(plan, s) != MOE_OK) return MOE_ERR_HIP;
-  if (launch_route_assign(plan->d, plan->idx, plan->work, s) != hipSuccess) return MOE_ERR_HIP;
+  CaptureId now;
+  moe_status st = capture_of(s, &now);
+  if (st != MOE_OK) return st;
+  if (holds(plan, plan->assigned, plan->assign_capture, now)) return MOE_OK;
+  st = scan_in(plan, now, s);
+  if (st != MOE_OK) return st;
+  // Recorded for a routing that has run: the ids of the latest route.
+  const int32_t* idx = now != 0 && plan->route_capture == 0 ? nullptr : plan->idx;
+  if (launch_route_assign(plan->d, idx, plan->work, s) != hipSuccess) return MOE_ERR_HIP;
   plan->assigned = true;
+  plan->assign_capture = now;
   return MOE_OK;
 }
 
@@ -242,10 +281,8 @@ moe_status moe_plan_create(const moe_config* cfg, moe_plan** out) {
   p->layout = moe::make_layout(d);
   p->idx = nullptr;
   p->ws = nullptr;
-  p->routed = false;
-  p->scanned = false;
-  p->scan_capture = 0;
-  p->assigned = false;
+  p->routed = p->finished = p->scanned = p->assigned = false;
+  p->route_capture = p->scan_capture = p->assign_capture = 0;
   p->timer = nullptr;
   *out = p;
   return MOE_OK;
@@ -353,18 +390,15 @@ moe_status moe_route_plan(moe_plan* plan, const int32_t* topk_idx, void* workspa
   const moe::TimerScope timing(plan);
   if (plan->d.T > 0 && (!topk_idx || !moe::aligned(topk_idx, 4))) return MOE_ERR_INVALID_ARGUMENT;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  plan->routed = false;
-  plan->assigned = false;
-  plan->idx = topk_idx;
-  plan->ws = workspace;
-  plan->work = moe::bind_work(plan->layout, workspace);
-  plan->scanned = false;
+  moe::CaptureId now;
+  const moe_status st = moe::capture_of(s, &now);
+  if (st != MOE_OK) return st;
+  moe::bind_routing(plan, topk_idx, workspace, now);
   if (moe::launch_route_count(plan->d, topk_idx, plan->work, s) != hipSuccess) return MOE_ERR_HIP;
   plan->routed = true;
   // Small single-hop plans leave the scan to the gather (and to whoever reads
   // the plan arrays before it).
-  if (!plan->d.fused_scan && moe::ensure_scanned(plan, s) != MOE_OK) return MOE_ERR_HIP;
-  return MOE_OK;
+  return plan->d.fused_scan ? MOE_OK : moe::scan_in(plan, now, s);
 }
 
 moe_status moe_route_plan_static(moe_plan* plan, const int32_t* topk_idx, void* stream) {
@@ -390,21 +424,19 @@ moe_status moe_pipeline(moe_plan* plan, const int32_t* topk_idx, void* workspace
     return MOE_ERR_INVALID_ARGUMENT;
   if (plan->d.T == 0) return moe_route_plan(plan, topk_idx, workspace, stream);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  plan->routed = false;
-  plan->assigned = false;
-  plan->idx = topk_idx;
-  plan->ws = workspace;
-  plan->work = moe::bind_work(plan->layout, workspace);
+  moe::CaptureId now;
+  const moe_status st = moe::capture_of(s, &now);
+  if (st != MOE_OK) return st;
+  moe::bind_routing(plan, topk_idx, workspace, now);
   // Every launch zeroes the counters first (one small kernel): a caller's
   // workspace may hold anything, a reused allocation included.
-  if (moe::launch_counters_clear(plan->d, plan->work, s) != hipSuccess) return MOE_ERR_HIP;
+  if (moe::launch_counters_clear(plan->d, topk_idx, plan->work, s) != hipSuccess)
+    return MOE_ERR_HIP;
   if (moe::launch_pipeline(plan->d, topk_idx, x, recv, topk_w, out, out_dtype == MOE_OUT_F32,
                            plan->work, s) != hipSuccess)
     return MOE_ERR_HIP;
-  plan->routed = true;
-  plan->scanned = true;
-  plan->scan_capture = 0;
-  plan->assigned = true;
+  plan->routed = plan->finished = plan->scanned = plan->assigned = true;
+  plan->scan_capture = plan->assign_capture = now;
   return MOE_OK;
 }
 
@@ -417,16 +449,18 @@ moe_status moe_dispatch(moe_plan* plan, const uint16_t* x, uint16_t* recv, uint1
   if (!x || !recv || !moe::aligned(x, 16) || !moe::aligned(recv, 16)) return MOE_ERR_INVALID_ARGUMENT;
   if (plan->d.dedup && (!staging || !moe::aligned(staging, 16))) return MOE_ERR_INVALID_ARGUMENT;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (!plan->d.dedup) {
-    if (moe::launch_gather(plan->d, plan->idx, x, recv, plan->work, s) != hipSuccess)
-      return MOE_ERR_HIP;
-    plan->assigned = true;
-    return MOE_OK;
-  }
-  if (moe::ensure_scanned(plan, s) != MOE_OK) return MOE_ERR_HIP;
+  moe::CaptureId now;
+  const moe_status st = moe::capture_of(s, &now);
+  if (st != MOE_OK) return st;
+  if (plan->d.dedup && moe::scan_in(plan, now, s) != MOE_OK) return MOE_ERR_HIP;
+  const hipError_t e =
+      plan->d.dedup
+          ? moe::launch_dedup_dispatch(plan->d, plan->idx, x, staging, recv, plan->work, s)
+          : moe::launch_gather(plan->d, plan->idx, x, recv, plan->work, s);
+  if (e != hipSuccess) return MOE_ERR_HIP;
   plan->assigned = true;
-  return moe::from_hip(
-      moe::launch_dedup_dispatch(plan->d, plan->idx, x, staging, recv, plan->work, s));
+  plan->assign_capture = now;
+  return MOE_OK;
 }
 
 moe_status moe_combine(moe_plan* plan, const uint16_t* y, const float* topk_w, void* out,
@@ -483,13 +517,17 @@ moe_status moe_dispatch_fp8(moe_plan* plan, const uint16_t* x, uint8_t* recv8, f
   hipStream_t s = static_cast<hipStream_t>(stream);
   // small single-hop plans with up to 64 experts: the fp8 gather scans the
   // tile counts itself
-  if (!moe::fp8_fused_scan(plan->d) && moe::ensure_scanned(plan, s) != MOE_OK) return MOE_ERR_HIP;
+  moe::CaptureId now;
+  const moe_status st = moe::capture_of(s, &now);
+  if (st != MOE_OK) return st;
+  if (!moe::fp8_fused_scan(plan->d) && moe::scan_in(plan, now, s) != MOE_OK) return MOE_ERR_HIP;
   const hipError_t e =
       plan->d.dedup ? moe::launch_stage_fp8(plan->d, plan->idx, x, staging8, staging_scale, recv8,
                                             recv_scale, plan->work, s)
                     : moe::launch_gather_fp8(plan->d, plan->idx, x, recv8, recv_scale, plan->work, s);
   if (e != hipSuccess) return MOE_ERR_HIP;
   plan->assigned = true;
+  plan->assign_capture = now;
   return MOE_OK;
 }
 

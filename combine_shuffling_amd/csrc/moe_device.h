@@ -67,6 +67,21 @@ __device__ __forceinline__ void token_slots(const Dims& d, const Work& w,
   for (int j = 0; j < KMAX; ++j) slot[j] = (j < d.k && l[j] >= 0) ? base[j] + l[j] : -1;
 }
 
+// Notes in the workspace where the ids of its latest route are, for an assign
+// that was recorded into a graph: the ids of the route it was recorded after
+// may be gone when it is replayed.
+__device__ __forceinline__ void note_ids(const Dims& d, const Work& w, const int32_t* idx) {
+  *reinterpret_cast<const int32_t**>(w.ctrl + kCtrlIdx) = idx;
+  w.ctrl[kCtrlSlots] = d.T * d.k;
+}
+
+// The ids noted; null where they are those of a batch of another size (another
+// plan's, on a workspace that plans share).
+__device__ __forceinline__ const int32_t* noted_ids(const Dims& d, const Work& w) {
+  const int32_t* idx = *reinterpret_cast<const int32_t* const*>(w.ctrl + kCtrlIdx);
+  return w.ctrl[kCtrlSlots] == d.T * d.k ? idx : nullptr;
+}
+
 // Staging row feeding every slot of token t (node deduplication): the first
 // slot of a node owns the row (tile base of its forwarder plus its rank),
 // later slots of the same node share it; -1 for a dropped slot.

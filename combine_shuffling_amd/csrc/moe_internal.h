@@ -36,6 +36,8 @@ constexpr int kFusedScanInts = 4096;
 
 // ctrl words at the start of the workspace.
 constexpr int kCtrlStaged = 1;     // D, staging rows used
+constexpr int kCtrlIdx = 2;        // address of the ids of the latest route (two words)
+constexpr int kCtrlSlots = 4;      // how many they are (T * k)
 constexpr int kCtrlWords = 64;
 
 // Banded pipeline: counters in Work::pipe, each in a slot of its own
@@ -141,6 +143,7 @@ hipError_t static_workspace(void** out);
 // route_count, and route_scan (one block per band).
 hipError_t launch_route_count(const Dims& d, const int32_t* idx, const Work& w, hipStream_t s);
 hipError_t launch_route_scan(const Dims& d, const Work& w, hipStream_t s);
+// idx null: those of the latest route on the workspace when the launch runs.
 hipError_t launch_route_assign(const Dims& d, const int32_t* idx, const Work& w, hipStream_t s);
 hipError_t launch_traffic(const Dims& d, const int32_t* idx, const Work& w, hipStream_t s);
 
@@ -166,8 +169,8 @@ hipError_t launch_combine_hier(const Dims& d, const uint16_t* y,
 hipError_t launch_pipeline(const Dims& d, const int32_t* idx, const uint16_t* x, uint16_t* recv,
                            const float* wts, void* out, bool out_f32, const Work& w,
                            hipStream_t s);
-// Zeroes the pipeline's counters in a workspace.
-hipError_t launch_counters_clear(const Dims& d, const Work& w, hipStream_t s);
+// Zeroes the pipeline's counters in a workspace, and notes its ids there.
+hipError_t launch_counters_clear(const Dims& d, const int32_t* idx, const Work& w, hipStream_t s);
 // fp8 payload (OCP E4M3 codes, one power-of-two scale per 128-element block).
 hipError_t launch_gather_fp8(const Dims& d, const int32_t* idx, const uint16_t* x, uint8_t* recv8,
                              float* rscale, const Work& w, hipStream_t s);

@@ -8,6 +8,8 @@
 #include "moe_internal.h"
 
 namespace moe {
+typedef unsigned long long CaptureId;
+
 // Event pairs of moe_plan_timing and the kernel of each recorded launch.
 struct LaunchTimer {
   std::vector<hipEvent_t> start, stop;
@@ -26,9 +28,11 @@ struct moe_plan {
   void* ws;
   moe::Work work;
   bool routed;     // route_count has been launched for the bound routing
+  bool finished;   // by a launch that scans and assigns too (moe_pipeline)
   bool scanned;    // route_scan has been launched for it (tile bases, offsets, status)
-  unsigned long long scan_capture;  // the stream capture that recorded it (0: none, it has run)
   bool assigned;   // slot_of / row_src (and stage_of / stage_src) are final
+  // The stream captures that recorded these (0: none, they were launched).
+  moe::CaptureId route_capture, scan_capture, assign_capture;
   moe::LaunchTimer* timer;  // per-launch timing, or null
 };
 
@@ -49,10 +53,16 @@ struct TimerScope {
   ~TimerScope() { tl_timer = prev; }
 };
 
+// The capture that stream s records into (0: none).
+moe_status capture_of(hipStream_t s, CaptureId* id);
+
+// A scan or an assign recorded into a graph counts in that capture only.  A
+// capture on a plan that was routed outside of it records its own, so that a
+// graph replayed after another route of the plan computes with that route.
+// And where the route itself was recorded, every replay routes anew, so that
+// each call outside of the graph does them again.
+//
 // Launches the plan's scan if the route left it to the gather (small plans).
-// A scan recorded into a graph counts in that capture only; and a capture on a
-// plan whose route leaves the scan out records one, so that a graph replayed
-// after another route of the plan reads that route's offsets.
 moe_status ensure_scanned(moe_plan* plan, hipStream_t s);
 // Makes slot_of / row_src (and the staging arrays) final when no dispatch
 // has done it since the last route.

@@ -203,8 +203,9 @@ __global__ __launch_bounds__(kBlock) void pipeline_kernel(Dims d, const int32_t*
   }
 }
 
-__global__ void counters_clear_kernel(int32_t* pipe, int n) {
-  for (int i = threadIdx.x; i < n; i += blockDim.x) pipe[i] = 0;
+__global__ void counters_clear_kernel(Dims d, const int32_t* idx, Work w, int n) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) w.pipe[i] = 0;
+  if (threadIdx.x == 0) note_ids(d, w, idx);
 }
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
@@ -290,9 +291,9 @@ hipError_t launch_pipeline(const Dims& d, const int32_t* idx, const uint16_t* x,
   return by_topk<PipelineLaunch>(d.k, d, idx, x, recv, wts, out, out_f32, w, s);
 }
 
-hipError_t launch_counters_clear(const Dims& d, const Work& w, hipStream_t s) {
-  return launch(MOE_KERNEL_COUNTERS_CLEAR, counters_clear_kernel, dim3(1), dim3(kBlock), 0, s,
-                w.pipe, (kPipeHead + 3 * d.nbands) * kPipeSlot);
+hipError_t launch_counters_clear(const Dims& d, const int32_t* idx, const Work& w, hipStream_t s) {
+  return launch(MOE_KERNEL_COUNTERS_CLEAR, counters_clear_kernel, dim3(1), dim3(kBlock), 0, s, d,
+                idx, w, (kPipeHead + 3 * d.nbands) * kPipeSlot);
 }
 
 }  // namespace moe

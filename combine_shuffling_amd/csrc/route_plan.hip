@@ -55,6 +55,7 @@ __global__ __launch_bounds__(kPlanBlock) void route_count_kernel(Dims d,
   __shared__ int s_frun[MOE_MAX_EXPERTS];  // tile's staging rows per key so far (fkeys <= 1024)
   __shared__ int s_node[MOE_MAX_EXPERTS];  // destination node of each expert (dedup)
   __shared__ int s_bad;
+  if (blockIdx.x == 0 && threadIdx.x == 0) note_ids(d, w, idx);
   count_tile<KMAX>(d, idx, w, blockIdx.x, CountLds{s_mask, s_pre, s_run, s_frun, s_node, &s_bad});
 }
 
@@ -74,13 +75,16 @@ __global__ __launch_bounds__(kScanBlock) void route_scan_kernel(Dims d, Work w) 
 }
 
 // Finishes the plan one token per thread (slot_of, row_src; with dedup
-// stage_of, stage_src) for consumers that run without a dispatch.
+// stage_of, stage_src) for consumers that run without a dispatch.  idx null:
+// the ids noted in the workspace.
 template <int KMAX>
 __global__ __launch_bounds__(kPlanBlock) void route_assign_kernel(Dims d,
                                                                   const int32_t* __restrict__ idx,
                                                                   Work w) {
   const int t = blockIdx.x * kPlanBlock + threadIdx.x;
   if (t >= d.T) return;
+  if (idx == nullptr) idx = noted_ids(d, w);
+  if (idx == nullptr) return;
   const int64_t at = (int64_t)t * d.k;
   const uint32_t rows = (uint32_t)(d.T * d.k);
   int slot[KMAX];

@@ -53,6 +53,17 @@
  * null stream).  A plan is not thread-safe; calls on one workspace that
  * overlap in time (different streams without ordering) race.
  *
+ * Graphs.  Every call but moe_plan_read can be captured.  The plan's state on
+ * the host follows what has run, not what is only recorded: a call recorded on
+ * a plan that was routed outside of the capture records what it needs of the
+ * plan (scan, slot arrays) with it, so that a graph replayed after another
+ * moe_route_plan of the plan, on the same workspace, computes with that
+ * routing; and on a plan whose route was recorded, a call outside of the graph
+ * takes the routing of its last replay, of which there has to be one.  Like
+ * every other argument, the topk_idx of the route is baked into a recorded
+ * moe_dispatch or moe_dispatch_fp8: routes between the replays of those put
+ * their ids into the same buffer.
+ *
  * Bands.  With band_tokens = B > 0 and B < T the batch is cut into
  * nb = ceil(T / B) bands; band b holds tokens [b*B, min((b+1)*B, T)) and owns
  * receive rows [b*B*k, min((b+1)*B, T)*k), laid out inside like a whole

@@ -1,0 +1,177 @@
+"""What a stream capture records of a plan, on the GPU: a scan or an assign that is only recorded
+does not count for eager calls, and a graph replayed after another route of its plan computes with
+that route."""
+
+import numpy as np
+import pytest
+import torch
+
+import combine_shuffling_amd as cs
+
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+PLANS = [
+    ("fused scan", 600, dict(num_ranks=4)),
+    ("dedup", 600, dict(num_ranks=4, ranks_per_node=2, node_dedup=True)),
+    ("banded", 600, dict(num_ranks=4, band_tokens=256)),
+    ("many tiles", 16300, dict(num_ranks=4)),      # the route scans by itself
+]
+E, K, H, N = 66, 3, 72, 40
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.device("cuda:0")
+
+
+class Calls:
+    """The calls that read a plan's slots or offsets, on inputs that stay the same."""
+
+    def __init__(self, T, kw, dev):
+        g = torch.Generator(device=dev)
+        g.manual_seed(T)
+        rand = lambda *s: torch.randn(*s, generator=g, device=dev)  # noqa: E731
+        self.T, self.kw, self.dev = T, kw, dev
+        self.x, self.grad_out = rand(T, H).bfloat16(), rand(T, H).bfloat16()
+        self.rows, self.w = rand(T * K, H).bfloat16(), rand(T, K)
+        self.weights = rand(E, N, H).bfloat16()
+        skew = torch.arange(E, device=dev) / 16
+        self.routes = [torch.topk(rand(T, E) + s, K, dim=1).indices.int().contiguous()
+                       for s in (0 * skew, skew)]
+        self.want = [self.all(self.plan().route(r)) for r in self.routes]
+        torch.cuda.synchronize()
+        for n in self.want[0]:
+            assert not torch.equal(self.want[0][n], self.want[1][n]), n
+
+    def plan(self):
+        return cs.Plan(self.T, H, E, K, **self.kw)
+
+    def routed(self, route):
+        # a workspace whose slots are out of range until something writes them
+        p = self.plan()
+        ws = torch.full((p.workspace_bytes,), 255, dtype=torch.uint8, device=self.dev)
+        return p.route(route, ws)
+
+    def all(self, p, which=("grad_x", "grad_y", "out", "y")):
+        r = {}
+        if "grad_x" in which:
+            r["grad_x"] = p.dispatch_backward(self.rows)
+        if "grad_y" in which:
+            r["grad_y"], r["grad_w"] = p.combine_backward(self.grad_out, self.rows, self.w)
+        if "out" in which:
+            r["out"] = p.combine(self.rows, self.w)
+        if "y" in which:
+            r["y"] = p.expert_linear(self.rows, self.weights)[0]
+        return r
+
+    def check(self, got, i, what):
+        bad = [n for n in got if not torch.equal(got[n], self.want[i][n])]
+        assert bad == [], (what, i, bad)
+
+
+def captured(call):
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    return graph, out
+
+
+@pytest.mark.parametrize("name,T,kw", PLANS, ids=[p[0] for p in PLANS])
+@pytest.mark.parametrize("which", ["grad_x", "grad_y", "out", "y"])
+@pytest.mark.parametrize("dispatched", [False, True], ids=["routed", "dispatched"])
+def test_call_captured_on_its_own(name, T, kw, which, dispatched, dev):
+    say(f"[graphs] {which} captured alone, {name}, dispatched before: {dispatched}")
+    c = Calls(T, kw, dev)
+    p = c.routed(c.routes[0])
+    if dispatched:
+        p.dispatch(c.x)
+    graph, outs = captured(lambda: [c.all(p, (which,)) for _ in range(2)])
+    c.check(c.all(p), 0, "eager, before the first replay")
+    for n, i in enumerate((0, 1, 0, 1)):
+        p.route(c.routes[i])
+        if n % 2:
+            c.check(c.all(p), i, "eager, before the replay")
+        for o in outs:
+            for t in o.values():
+                t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for o in outs:
+            c.check(o, i, "replayed")
+        c.check(c.all(p), i, "eager, after the replay")
+
+
+@pytest.mark.parametrize("name,T,kw", PLANS, ids=[p[0] for p in PLANS])
+def test_captured_dispatch_does_not_count_for_eager_calls(name, T, kw, dev):
+    say(f"[graphs] dispatch captured alone, {name}")
+    c = Calls(T, kw, dev)
+    p = c.routed(c.routes[0])
+    graph, (recv, _) = captured(lambda: p.dispatch(c.x))
+    c.check(c.all(p), 0, "eager, before the first replay")
+    want = recv.clone().zero_()
+    p.dispatch(c.x, want)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(recv, want)
+
+
+@pytest.mark.parametrize("name,T,kw", PLANS, ids=[p[0] for p in PLANS])
+@pytest.mark.parametrize("inside", ["route", "route and dispatch", "everything"])
+def test_captured_route(name, T, kw, inside, dev):
+    # The route itself is recorded and replayed on other routings: eager calls between the replays
+    # take the routing of the last one.
+    say(f"[graphs] {inside} captured, {name}")
+    c = Calls(T, kw, dev)
+    ids = c.routes[0].clone()
+    p = c.routed(ids)
+
+    def call():
+        p.route(ids)
+        if inside != "route":
+            p.dispatch(c.x)
+        return c.all(p) if inside == "everything" else {}
+
+    graph, outs = captured(call)
+    for n, i in enumerate((0, 1, 0, 1, 1, 0)):
+        ids.copy_(c.routes[i])
+        for t in outs.values():
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check(outs, i, "replayed")
+        for _ in range(1 + n % 2):
+            c.check(c.all(p), i, "eager, after the replay")
+    # and an eager route of the plan ends that
+    p.route(c.routes[1])
+    for _ in range(2):
+        c.check(c.all(p), 1, "eager, after a route")
+
+
+@pytest.mark.parametrize("band", [0, 256])
+def test_captured_pipeline(band, dev):
+    # A pipeline routes and finishes its plan in its own launch, recorded or not.
+    T, H2 = 600, 64
+    g = torch.Generator(device=dev)
+    g.manual_seed(1)
+    x = torch.randn(T, H2, generator=g, device=dev).bfloat16()
+    w = torch.randn(T, K, generator=g, device=dev)
+    rows = torch.randn(T * K, H2, generator=g, device=dev).bfloat16()
+    routes = [torch.topk(torch.randn(T, E, generator=g, device=dev), K, dim=1).indices.int().contiguous()
+              for _ in range(2)]
+    plan = lambda: cs.Plan(T, H2, E, K, 4, band_tokens=band)  # noqa: E731
+    want = [plan().route(r).dispatch_backward(rows) for r in routes]
+    ids = routes[0].clone()
+    p = plan().route(ids)
+    graph, (recv, out) = captured(lambda: p.pipeline(ids, x, w))
+    for i in (0, 1, 0, 1):
+        ids.copy_(routes[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        for _ in range(2):
+            assert torch.equal(p.dispatch_backward(rows), want[i])
+            assert np.array_equal(p.read("slot_of"), plan().route(routes[i]).read("slot_of"))
