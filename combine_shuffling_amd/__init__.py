@@ -362,28 +362,34 @@ class Plan:
         return out
 
     # -- moe_router
-    def _router_config(self, score: str, renormalise: bool, nodes_per_token: int, scale: float):
+    def _router_config(self, score: str, renormalise: bool, nodes_per_token: int, scale: float,
+                       key: str = "logit"):
         if score not in _abi.SCORE:
             raise ValueError(f"score must be one of {tuple(_abi.SCORE)}")
+        if key not in _abi.ROUTER_KEY:
+            raise ValueError(f"key must be one of {tuple(_abi.ROUTER_KEY)}")
         return ctypes.byref(_abi.RouterConfig(_abi.SCORE[score], bool(renormalise), nodes_per_token,
-                                              scale))
+                                              scale, _abi.ROUTER_KEY[key]))
 
     @_on_stream
     def router(self, logits: torch.Tensor, bias: torch.Tensor | None = None,
                score: str = "softmax", renormalise: bool = True, scale: float = 1.0,
                nodes_per_token: int = 0, topk_idx: torch.Tensor | None = None,
-               topk_w: torch.Tensor | None = None):
+               topk_w: torch.Tensor | None = None, key: str = "logit"):
         """Gate logits [T, E] (float32 or bf16) -> (topk_idx int32 [T, k], topk_w float32 [T, k]).
 
-        The k experts of the largest logit + bias (bias: float32 [E], for the choice only), in
+        The k experts of the largest key + bias (bias: float32 [E], for the choice only), in
         descending order, ties to the lower id; nodes_per_token m > 0 allows the experts of the
-        token's m best nodes only.  Weights: scale * softmax or sigmoid of the logits, over the
-        sum of the selected ones with renormalise.  The plan need not be routed."""
+        token's m best nodes only, by the sum of a node's two largest.  key: "logit", or "score"
+        for the softmax or sigmoid of the logits; a bias belongs to the one it was adjusted for
+        (DeepSeek-V3's routing: score="sigmoid", key="score").  Weights: scale * softmax or sigmoid
+        of the logits, over the sum of the selected ones with renormalise.  The plan need not be
+        routed."""
         dev = logits.device
         _need(logits, (self.T, self.E), (torch.float32, torch.bfloat16), "logits", dev)
         if bias is not None:
             _need(bias, (self.E,), _F32, "bias", dev)
-        cfg = self._router_config(score, renormalise, nodes_per_token, scale)
+        cfg = self._router_config(score, renormalise, nodes_per_token, scale, key)
         if topk_idx is not None or topk_w is not None:
             _apart((topk_idx, topk_w), (logits, bias))
         topk_idx = _out(topk_idx, (self.T, self.k), torch.int32, "topk_idx", dev)
@@ -641,10 +647,10 @@ def pipeline(plan: Plan, topk_idx: torch.Tensor, x: torch.Tensor, topk_w: torch.
 
 def router(plan: Plan, logits: torch.Tensor, bias=None, score: str = "softmax",
            renormalise: bool = True, scale: float = 1.0, nodes_per_token: int = 0, topk_idx=None,
-           topk_w=None, stream=None):
+           topk_w=None, stream=None, key: str = "logit"):
     """moe_router: returns (topk_idx [T, k] int32, topk_w [T, k] float32)."""
     return plan.router(logits, bias, score, renormalise, scale, nodes_per_token, topk_idx, topk_w,
-                       stream=stream)
+                       key, stream=stream)
 
 
 def router_backward(plan: Plan, logits: torch.Tensor, topk_idx: torch.Tensor, grad_w: torch.Tensor,

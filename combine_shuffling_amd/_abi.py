@@ -31,8 +31,9 @@ MAX_TOPK = 16
 OUT_BF16 = 0
 OUT_F32 = 1
 
-# moe_layer.h: moe_score, moe_activation
+# moe_layer.h: moe_score, moe_router_key, moe_activation
 SCORE = dict(softmax=0, sigmoid=1)
+ROUTER_KEY = dict(logit=0, score=1)
 ACTIVATION = dict(none=0, relu=1, silu=2, gelu=3, swiglu=4, geglu=5)
 GATED = ("swiglu", "geglu")
 
@@ -61,6 +62,7 @@ class RouterConfig(ctypes.Structure):
         ("renormalise", ctypes.c_int32),
         ("nodes_per_token", ctypes.c_int32),
         ("scale", ctypes.c_float),
+        ("key", ctypes.c_int32),
     ]
 
 

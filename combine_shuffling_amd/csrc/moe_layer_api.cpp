@@ -26,6 +26,7 @@ int64_t fewest_experts(const Dims& d, int32_t m) {
 moe_status check_router(const moe_plan* plan, const moe_router_config* c, int32_t dtype) {
   if (!plan || !c || !is_dtype(dtype)) return MOE_ERR_INVALID_ARGUMENT;
   if (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARGUMENT;
+  if (c->key != MOE_KEY_LOGIT && c->key != MOE_KEY_SCORE) return MOE_ERR_INVALID_ARGUMENT;
   if (!std::isfinite(c->scale)) return MOE_ERR_INVALID_ARGUMENT;
   const Dims& d = plan->d;
   if (c->nodes_per_token < 0 || c->nodes_per_token > d.N) return MOE_ERR_INVALID_ARGUMENT;

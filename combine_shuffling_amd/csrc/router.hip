@@ -3,7 +3,8 @@
 //
 // A token has a wave, or, in large batches, 16 lanes of one; lane l of L
 // holds the logits of experts i * L + l, so the row is read once, coalesced,
-// and stays in registers.  Choice: every key becomes an unsigned number of the
+// and stays in registers.  Choice: every key (the logit or the score, plus the
+// bias) becomes an unsigned number of the
 // same order; a lane sorts its keys into short lists, and k rounds find the
 // largest head with a maximum over the lanes by data-parallel moves.
 //
@@ -221,8 +222,26 @@ __device__ __forceinline__ float selected_score(const moe_router_config& c, floa
   return row_sum > 0.0f ? exp_below(x, row_max) / row_sum : 0.0f;
 }
 
+// Softmax statistics of a row of which this lane holds V logits in v, which
+// become exp(logit - row_max); experts past E and NaN have -infinity.
+template <int V, int L>
+__device__ __forceinline__ void row_statistics(float (&v)[V], float& row_max, float& row_sum) {
+  row_max = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < V; ++i) row_max = fmaxf(row_max, v[i]);
+  row_max = fold_max<L>(row_max);
+  row_sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    v[i] = exp_below(v[i], row_max);
+    row_sum += v[i];
+  }
+  row_sum = fold_sum<L>(row_sum);
+}
+
 // A token has L lanes (16 or 64), a lane V logits (a power of two >= E / L).
-template <int V, int L, bool F32>
+// BY_SCORE: c.key is MOE_KEY_SCORE.
+template <int V, int L, bool F32, bool BY_SCORE>
 __global__ __launch_bounds__(kRouterWaves * kWave) void router_kernel(
     Dims d, moe_router_config c, const void* __restrict__ logits, const float* __restrict__ bias,
     int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
@@ -246,6 +265,22 @@ __global__ __launch_bounds__(kRouterWaves * kWave) void router_kernel(
     uint32_t(&key)[V] = lists.key;
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = load_logit<F32>(logits, t * d.E + min(i * L + lane, d.E - 1));
+    float row_max = 0.0f, row_sum = 0.0f;
+    if constexpr (BY_SCORE) {
+      float p[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) p[i] = i * L + lane < d.E ? no_nan(v[i]) : -INFINITY;
+      if (c.score == MOE_SCORE_SOFTMAX) {
+        row_statistics<V, L>(p, row_max, row_sum);
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] /= row_sum;  // > 0 where a logit is above -infinity
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] = sigmoid(p[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = v[i] > -INFINITY ? p[i] : v[i];  // NaN stays NaN
+    }
     if (bias != nullptr) {
       float x[V];
 #pragma unroll
@@ -315,22 +350,16 @@ __global__ __launch_bounds__(kRouterWaves * kWave) void router_kernel(
     }
     const bool has = lane < d.k;
     float xs = key_value(taken);  // without a bias the key is the logit
-    if (bias != nullptr) xs = no_nan(load_logit<F32>(logits, t * d.E + id));
-    float row_max = 0.0f, row_sum = 0.0f;
-    if (c.score == MOE_SCORE_SOFTMAX && !c.renormalise) {
+    if (BY_SCORE || bias != nullptr) xs = no_nan(load_logit<F32>(logits, t * d.E + id));
+    if (!BY_SCORE && c.score == MOE_SCORE_SOFTMAX && !c.renormalise) {
       // loaded again, so that the rounds above need not hold them
-      row_max = -INFINITY;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int e = i * L + lane;
         v[i] = no_nan(load_logit<F32>(logits, t * d.E + min(e, d.E - 1)));
         v[i] = e < d.E ? v[i] : -INFINITY;
-        row_max = fmaxf(row_max, v[i]);
       }
-      row_max = fold_max<L>(row_max);
-#pragma unroll
-      for (int i = 0; i < V; ++i) row_sum += exp_below(v[i], row_max);
-      row_sum = fold_sum<L>(row_sum);
+      row_statistics<V, L>(v, row_max, row_sum);
     }
     const float p = selected_score(c, xs, has, row_max, row_sum);
     if (has && (L == kWave || at < d.T)) {
@@ -450,15 +479,19 @@ hipError_t launch_router(const Dims& d, const moe_router_config& c, const void* 
     return launch(MOE_KERNEL_ROUTER, kernel, router_grid(d, kWave / lanes),
                   dim3(kRouterWaves * kWave), 0, s, d, c, logits, bias, topk_idx, topk_w);
   };
+  auto by_type = [&](auto v, auto lanes) {
+    constexpr int V = decltype(v)::value, L = decltype(lanes)::value;
+    if (c.key == MOE_KEY_SCORE)
+      return go(f32 ? router_kernel<V, L, true, true> : router_kernel<V, L, false, true>, L);
+    return go(f32 ? router_kernel<V, L, true, false> : router_kernel<V, L, false, false>, L);
+  };
   if (d.T > kWholeWave && d.E <= 256 && (c.nodes_per_token == 0 || d.N <= 16)) {
-    if (d.E <= 64) return go(f32 ? router_kernel<4, 16, true> : router_kernel<4, 16, false>, 16);
-    if (d.E <= 128) return go(f32 ? router_kernel<8, 16, true> : router_kernel<8, 16, false>, 16);
-    return go(f32 ? router_kernel<16, 16, true> : router_kernel<16, 16, false>, 16);
+    constexpr std::integral_constant<int, 16> lanes;
+    if (d.E <= 64) return by_type(std::integral_constant<int, 4>(), lanes);
+    if (d.E <= 128) return by_type(std::integral_constant<int, 8>(), lanes);
+    return by_type(std::integral_constant<int, 16>(), lanes);
   }
-  return by_experts(d.E, [&](auto v) {
-    constexpr int V = decltype(v)::value;
-    return go(f32 ? router_kernel<V, kWave, true> : router_kernel<V, kWave, false>, kWave);
-  });
+  return by_experts(d.E, [&](auto v) { return by_type(v, std::integral_constant<int, kWave>()); });
 }
 
 hipError_t launch_router_grad(const Dims& d, const moe_router_config& c, const void* logits,

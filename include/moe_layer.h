@@ -42,6 +42,11 @@ typedef enum moe_score {
   MOE_SCORE_SIGMOID = 1  /* p = 1 / (1 + exp(-logit))           */
 } moe_score;
 
+typedef enum moe_router_key {
+  MOE_KEY_LOGIT = 0, /* experts are chosen by their logits             */
+  MOE_KEY_SCORE = 1  /* by their scores p, as float32 computes them    */
+} moe_router_key;
+
 typedef struct moe_router_config {
   int32_t score;           /* moe_score                                                  */
   int32_t renormalise;     /* nonzero: the k selected scores are divided by their sum    */
@@ -49,12 +54,20 @@ typedef struct moe_router_config {
                               nodes (the plan's N = R / G nodes), a node's worth being the
                               float32 sum of its two largest keys; ties to the lower node */
   float scale;             /* the weights are multiplied by this                         */
+  int32_t key;             /* moe_router_key                                             */
 } moe_router_config;
 
-/* Router: key[e] = logit[e] (+ bias[e], added in float32); the experts of the
- * k largest keys, in descending order, ties to the lower id, are topk_idx[t];
- * topk_w[t, j] = scale * p[id_j] (/ sum over the k selected p).  The bias only
- * takes part in the choice (a balancing bias); p is of the logits alone.
+/* Router: key[e] = logit[e] or p[e] (+ bias[e], added in float32); the experts
+ * of the k largest keys, in descending order, ties to the lower id, are
+ * topk_idx[t]; topk_w[t, j] = scale * p[id_j] (/ sum over the k selected p).
+ * The bias only takes part in the choice; p is of the logits alone.
+ * Scores rise with the logits, so that without a bias and a limit of the nodes
+ * both keys choose alike, up to scores that float32 rounds to one value.  With
+ * either they do not: a bias is added to what it was adjusted for.  Balancing
+ * without an auxiliary loss adjusts it for the scores, and the node-limited
+ * routing of DeepSeek-V3 sums a node's two largest biased sigmoid scores:
+ * MOE_SCORE_SIGMOID with MOE_KEY_SCORE.
+ * With either key a logit of -infinity has the key -infinity.
  * A NaN key ranks below -infinity, and a NaN logit has p = 0.  Where all the
  * scores of a sum are 0 (all logits -infinity), the weights are 0.  An
  * infinite maximum logit stands for the limit: p is shared by the logits that
@@ -63,7 +76,7 @@ typedef struct moe_router_config {
  * element; bias: [E] float32 or NULL; topk_idx [T, k] int32 and topk_w [T, k]
  * float32, 4-byte aligned, as moe_route_plan and moe_combine take them.  The
  * plan need not be routed.  Limits: with nodes_per_token m > 0, N <= 64 nodes.
- * Errors: INVALID_ARGUMENT (null or misaligned pointers, unknown score or
+ * Errors: INVALID_ARGUMENT (null or misaligned pointers, unknown score, key or
  * dtype, m < 0 or m > N, fewer than k experts on the m smallest nodes, a scale
  * that is not finite), UNSUPPORTED (N > 64 with m > 0), HIP. */
 moe_status moe_router(moe_plan* plan, const moe_router_config* cfg, const void* logits,
