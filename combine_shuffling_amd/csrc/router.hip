@@ -82,10 +82,11 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
 }
 
 // Folds f over every row of 16 lanes, by rotations, or over the wave (L: 16 or
-// 64); every lane gets its result.  The order is fixed, and the same bits
+// kWave); every lane gets its result.  The order is fixed, and the same bits
 // come out in every lane (the two operands of a rotation's step only swap).
 template <int L, typename T, typename F>
 __device__ __forceinline__ T fold(T v, T none, F f) {
+  static_assert(L == 16 || L == kWave);
   if constexpr (L == 16) {
     v = f(v, moved<kRowRor + 8>(none, v));
     v = f(v, moved<kRowRor + 4>(none, v));
@@ -396,20 +397,12 @@ __global__ __launch_bounds__(kRouterWaves * kWave) void router_grad_kernel(
     float p[V];
     float row_max = 0.0f, row_sum = 0.0f;
     if (whole) {
-      row_max = -INFINITY;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int e = i * kWave + lane;
         p[i] = e < d.E ? no_nan(load_logit<F32>(logits, t * d.E + e)) : -INFINITY;
-        row_max = fmaxf(row_max, p[i]);
       }
-      row_max = fold_max<true>(row_max);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        p[i] = exp_below(p[i], row_max);
-        row_sum += p[i];
-      }
-      row_sum = fold_sum<true>(row_sum);
+      row_statistics<V, kWave>(p, row_max, row_sum);
       const float inv = row_sum > 0.0f ? 1.0f / row_sum : 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) p[i] *= inv;
