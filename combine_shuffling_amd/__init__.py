@@ -507,7 +507,7 @@ class Plan:
 
     # -- moe_expert_linear_backward
     @_on_stream
-    def expert_linear_backward(self, grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
+    def expert_linear_backward(self, grad_y: torch.Tensor, x: torch.Tensor | None, w: torch.Tensor,
                                pre: torch.Tensor | None = None, activation: str = "none",
                                bias_grad: bool = False, x_grad: bool = True, w_grad: bool = True,
                                grad_w_dtype: torch.dtype = torch.bfloat16,
@@ -519,15 +519,17 @@ class Plan:
         grad_w_dtype, grad_bias [E, Z] float32), None for one that is not wanted.
 
         pre: what expert_linear stored, needed with an activation.  x_grad, w_grad, bias_grad say
-        which are wanted; grad_x, grad_w, grad_bias: tensors to write them to.  The gradient of the
-        residual is grad_y."""
+        which are wanted; grad_x, grad_w, grad_bias: tensors to write them to.  x is read for grad_w
+        only and may be None without it; w also says the sizes.  The gradient of the residual is
+        grad_y."""
         dev = self.device
         if dev is None:
             raise MoeError(_abi.ERR_PLAN_NOT_ROUTED, "expert_linear_backward")
         cfg, K, N, Z = self._expert_config(w, activation)
         rows = self.recv_rows
         _need(grad_y, (rows, N), _BF16, "grad_y", dev)
-        _need(x, (rows, K), _BF16, "x", dev)
+        if w_grad or x is not None:
+            _need(x, (rows, K), _BF16, "x", dev)
         if activation != "none":
             if pre is None:
                 raise ValueError("pre is needed with an activation")
@@ -551,7 +553,7 @@ class Plan:
         grad_x = _out(grad_x, (rows, K), torch.bfloat16, "grad_x", dev) if x_grad else None
         grad_w = _out(grad_w, (self.E, Z, K), grad_w_dtype, "grad_w", dev) if w_grad else None
         grad_bias = _out(grad_bias, (self.E, Z), torch.float32, "grad_bias", dev) if bias_grad else None
-        self._launch("moe_expert_linear_backward", dev, cfg, grad_y.data_ptr(), x.data_ptr(),
+        self._launch("moe_expert_linear_backward", dev, cfg, grad_y.data_ptr(), _addr(x),
                      w.data_ptr(), _addr(pre), _addr(grad_x), _addr(grad_w), code, _addr(grad_bias),
                      workspace.data_ptr())
         return grad_x, grad_w, grad_bias
@@ -680,7 +682,7 @@ def expert_linear(plan: Plan, x: torch.Tensor, w: torch.Tensor, bias=None, resid
                               stream=stream)
 
 
-def expert_linear_backward(plan: Plan, grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
+def expert_linear_backward(plan: Plan, grad_y: torch.Tensor, x: torch.Tensor | None, w: torch.Tensor,
                            pre=None, activation: str = "none", bias_grad: bool = False,
                            x_grad: bool = True, w_grad: bool = True,
                            grad_w_dtype: torch.dtype = torch.bfloat16, grad_x=None, grad_w=None,

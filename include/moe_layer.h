@@ -159,8 +159,9 @@ size_t moe_expert_backward_workspace_bytes(const moe_plan* plan, const moe_exper
  * activation grad_z is rounded to bf16 for the two products, which the matrix
  * cores take as bf16 (grad_bias sums it unrounded).  The residual's gradient is
  * grad_y.  grad_y: [T*k, N] bf16; pre: [T*k, Z] bf16 as moe_expert_linear
- * stored it (ignored without an activation); w_dtype: moe_out_dtype of grad_w;
- * workspace: 256-byte aligned.
+ * stored it (ignored without an activation); x is read for grad_w only and w
+ * for grad_x only, and may be NULL without it; w_dtype: moe_out_dtype of
+ * grad_w; workspace: 256-byte aligned.
  * Errors as moe_expert_linear. */
 moe_status moe_expert_linear_backward(moe_plan* plan, const moe_expert_config* cfg,
                                       const uint16_t* grad_y, const uint16_t* x, const uint16_t* w,
