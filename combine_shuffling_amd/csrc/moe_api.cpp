@@ -111,7 +111,7 @@ Work bind_work(const Layout& l, void* base) {
 
 moe_status capture_of(hipStream_t s, CaptureId* id) {
   *id = 0;
-  if (s == nullptr) return MOE_OK;  // the null stream is never captured
+  if (s == nullptr || s == hipStreamLegacy) return MOE_OK;  // the null stream is never captured
   hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
   CaptureId v = 0;
   if (hipStreamGetCaptureInfo(s, &status, &v) != hipSuccess) return MOE_ERR_HIP;

@@ -39,6 +39,8 @@ class Calls:
         self.x, self.grad_out = rand(T, H).bfloat16(), rand(T, H).bfloat16()
         self.rows, self.w = rand(T * K, H).bfloat16(), rand(T, K)
         self.weights = rand(E, N, H).bfloat16()
+        self.codes = torch.randint(0, 0x78, (T * K, H), generator=g, dtype=torch.uint8, device=dev)
+        self.scales = torch.ones(T * K, (H + 127) // 128, device=dev)
         skew = torch.arange(E, device=dev) / 16
         self.routes = [torch.topk(rand(T, E) + s, K, dim=1).indices.int().contiguous()
                        for s in (0 * skew, skew)]
@@ -56,7 +58,7 @@ class Calls:
         ws = torch.full((p.workspace_bytes,), 255, dtype=torch.uint8, device=self.dev)
         return p.route(route, ws)
 
-    def all(self, p, which=("grad_x", "grad_y", "out", "y")):
+    def all(self, p, which=("grad_x", "grad_y", "out", "y", "fp8", "hier")):
         r = {}
         if "grad_x" in which:
             r["grad_x"] = p.dispatch_backward(self.rows)
@@ -66,6 +68,10 @@ class Calls:
             r["out"] = p.combine(self.rows, self.w)
         if "y" in which:
             r["y"] = p.expert_linear(self.rows, self.weights)[0]
+        if "fp8" in which:
+            r["fp8"] = p.combine_fp8(self.codes, self.scales, self.w)
+        if "hier" in which and p.node_dedup:
+            r["hier"] = p.combine_hier(self.rows, self.w)
         return r
 
     def check(self, got, i, what):
@@ -81,10 +87,13 @@ def captured(call):
     return graph, out
 
 
-@pytest.mark.parametrize("name,T,kw", PLANS, ids=[p[0] for p in PLANS])
-@pytest.mark.parametrize("which", ["grad_x", "grad_y", "out", "y"])
+ALONE = [(w, *p) for w in ("grad_x", "grad_y", "out", "y", "fp8", "hier") for p in PLANS
+         if w != "hier" or "node_dedup" in p[2]]
+
+
+@pytest.mark.parametrize("which,name,T,kw", ALONE, ids=[f"{a[0]}-{a[1]}" for a in ALONE])
 @pytest.mark.parametrize("dispatched", [False, True], ids=["routed", "dispatched"])
-def test_call_captured_on_its_own(name, T, kw, which, dispatched, dev):
+def test_call_captured_on_its_own(which, name, T, kw, dispatched, dev):
     say(f"[graphs] {which} captured alone, {name}, dispatched before: {dispatched}")
     c = Calls(T, kw, dev)
     p = c.routed(c.routes[0])
