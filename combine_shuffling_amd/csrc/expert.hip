@@ -11,14 +11,18 @@
 // and a step's fragments are read from LDS while the previous step's are
 // multiplied; the loads run on from one tile to the next.
 //
-// What bounds it.  Products of large square matrices run into the power
-// limit: 8192^3 takes 870 to 940 us in all three directions (1.17 to 1.27
-// PFLOP/s, matrix cores busy 65% of the cycles at 1.9 GHz; the library's
-// product of the same matrices 777 us, 87% at 1.6 GHz).  The experts' products
-// add to that the traffic of the weights and rows, which costs time even
-// under the multiplications: 64 experts, 4096 tokens, top-8, 2048 -> 2 x 1024
-// takes 335 to 375 us, where one matrix of the same 275 GFLOP takes 250 and
-// the 0.87 GB that it reads and writes 180 at the rate of a copy.  Steps:
+// What bounds it.  Products of large square matrices: 8192^3 takes 870 to 940
+// us in all three directions (1.17 to 1.27 PFLOP/s, matrix cores busy 65% of
+// the cycles at 1.9 GHz; the library's product of the same matrices 777 us, 87%
+// at 1.6 GHz).  The experts' products take about the time of their operations
+// and that of their bytes, one after the other: 64 experts, 4096 tokens, top-8,
+// 2048 -> 2 x 1024 takes 335 to 370 us, where one matrix of the same 275 GFLOP
+// takes 250 and the 0.87 GB that it has to read and write 180 at the rate of a
+// copy.  Matrix cores are busy in 42% of its cycles (a Zipf batch 34%, both
+// gradients in one launch 43%) at 1.75 to 1.93 GHz, so it is memory time that is
+// not hidden, not power, that binds them: a CU holds one block (100 KiB of LDS),
+// no product runs while its waves load the residual and store y and pre, and the
+// operands come twice through L2 (1.3 GB read where 0.67 are needed).  Steps:
 // fragments read a step ahead of their products and reads that do not wait
 // for loads under way (8192^3 from 1220, 1159 and 1447 us to 883, 870 and
 // 877), tiles grouped by XCD (half of that: from 50% of L2 requests missing),
@@ -1076,8 +1080,8 @@ constexpr int kActRows = 8;   // rows at a time
 // One block per slot of kBiasRows rows and strip of 256 columns of grad_y.  A
 // thread owns 8 columns and every 8th row; the column sums of the block are
 // added in a fixed order.  gz is rounded to bf16, the type that both products
-// multiply, once and from float32.  Bound by HBM: 32768 rows of 2 x 1024 (335 MB) 62 us, 5.4
-// TB/s; 4084 rows of 1000 (24.5 MB) 10.4 us, of which any launch takes 4.
+// multiply, once and from float32.  Bound by HBM: 32768 rows of 2 x 1024 (335 MB) 70 us, 4.8
+// TB/s; 4084 rows of 1000 (24.5 MB) 11 us, of which any launch takes 4.
 __global__ __launch_bounds__(kActCols * kActRows) void expert_act_grad_kernel(
     ExpertDims x, const int32_t* __restrict__ off, const uint16_t* __restrict__ gy,
     const uint16_t* __restrict__ pre, uint16_t* __restrict__ gz, float* __restrict__ partial,

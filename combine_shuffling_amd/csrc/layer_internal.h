@@ -40,10 +40,10 @@ inline bool gated(int32_t act) { return act == MOE_ACT_SWIGLU || act == MOE_ACT_
 // Rows per slot of the partial bias sums, and the slots: expert e's of band b
 // start at off / kBiasRows + e + b * E (off: its first row), which leaves room
 // for the rows of every expert without knowing their counts on the host.  A
-// block of the activation's gradient takes one slot: 32 rows against 64 took
-// 1021 tokens of 1000 columns from 12.3 to 10.6 us and 4096 of 2 x 1024 from 66 to
-// 62, and the bias sums of a Zipf batch (one expert of 8192 rows) from 12.6 to 19.5;
-// 16 rows 9.2, 60.5 and 34.9.
+// block of the activation's gradient takes one slot.  Against 64 rows, 32 took
+// 14% off it for 4084 rows of 1000 columns (11 us) and 6% for 32768 of 2 x 1024 (70
+// us), and added half to the bias sums of a Zipf batch (one expert of 8192 rows: 12.6
+// to 19.5 us); 16 rows 25%, 8%, and 34.9 us.
 constexpr int kBiasRows = 32;
 inline int64_t bias_slots(const ExpertDims& x) {
   return x.rows / kBiasRows + (int64_t)x.bands * x.E;

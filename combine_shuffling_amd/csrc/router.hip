@@ -21,8 +21,14 @@
 // data-parallel moves, 18.8 with sorted lists, 17.4 with the nodes' experts
 // cleared through LDS instead of compared each round, 14.1 with 16 lanes a token,
 // whose rounds serve four tokens.  Few tokens wait for the chain of a token's
-// rounds: 5.0 us for 16, of which 4 are any launch's (the gradient's, which has no
-// rounds, take 4.0).  The gradient reads and writes 33.5 MB there: 9.3 us, 3.6 TB/s.
+// rounds: 5.1 us for 16, of which 4 are any launch's (the gradient's, which has no
+// rounds, take 4.0).  A choice by scores has their exponentials and quotients before
+// the rounds: 17.2 us there for the sigmoid and 17.6 for the softmax.
+// The gradient of renormalised weights reads the k selected logits of a token, one
+// by one, and writes its row, 16.8 MB there: 9.1 us, where the stores alone would
+// take 3.5.  It waits for the chain of a token's ids, logits and two folds, a token
+// a wave, and stores 4 bytes a lane.  That of a softmax over all experts reads the
+// rows too: 12.5 us, 2.7 TB/s.
 #include <algorithm>
 #include <type_traits>
 

@@ -43,7 +43,8 @@ constexpr int kDispatchGradWaves = 2;
 // grad_x[t] = sum over the slots j of grad_recv[row of (t, j)], in float32 in the
 // order of the slots.  All rows of a segment are loaded before the first is
 // added, so k * 1 KiB are under way a wave.  32768 tokens of 2048 bf16, top-6 (940
-// MB): 153 us, 6.1 TB/s; 128 tokens of 256, top-2: 4.0 us, which any launch takes.
+// MB): 152 us, 6.2 TB/s; 4096 of 2048 float32, top-8 (168 MB): 25.6 us; 128 of 256, top-2:
+// 2.5 us, a launch.
 // Wave-items [base, limit) of the batch (one launch of at most kMaxLaunchItems).
 template <int KMAX, bool F32>
 __global__ __launch_bounds__(kDispatchGradWaves * kWave) void dispatch_grad_kernel(
@@ -94,7 +95,9 @@ constexpr int kCombineGradBlocks = 1 << 20;  // tokens a launch at most; more go
 //   grad_y[row of (t, j)] = wts[t, j] * grad_out[t]
 //   grad_w[t, j] = sum over the columns of grad_out[t] * y[row of (t, j)]
 // grad_out is read once for both.  4096 tokens of 2048 float32, top-8 (302 MB): 61 us,
-// 5.0 TB/s; 16384 of 7168, top-8 (4.0 GB): 798 us, 5.0 TB/s.  Other numbers of waves a
+// 5.0 TB/s; 16384 of 7168, top-8 (4.0 GB): 798 us, 5.0 TB/s.  Rows of fewer than 2048
+// columns leave waves of their block idle: 16384 tokens of 64, top-8 (36 MB) 78 us, of 256 (143
+// MB) 81, bound by their blocks.  Other numbers of waves a
 // token, and plain instead of streaming loads and stores, measured equal or worse.
 template <int KMAX, bool F32>
 __global__ __launch_bounds__(kCombineGradWaves * kWave) void combine_grad_kernel(
