@@ -122,10 +122,10 @@ moe_status capture_of(hipStream_t s, CaptureId* id) {
 namespace {
 
 // Whether a scan or an assign holds for a call in capture `now`: it was done
-// in the same capture, or outside of any on a plan routed outside of any.
+// in the same capture, or, for a call outside of any, wherever the route was
+// (outside of any too, or in one graph with the route).
 bool holds(const moe_plan* plan, bool done, CaptureId in, CaptureId now) {
-  if (plan->finished && (now == 0 || now == plan->route_capture)) return true;
-  return done && in == now && (now != 0 || plan->route_capture == 0);
+  return done && in == (now != 0 ? now : plan->route_capture);
 }
 
 moe_status scan_in(moe_plan* plan, CaptureId now, hipStream_t s) {
@@ -140,7 +140,7 @@ moe_status scan_in(moe_plan* plan, CaptureId now, hipStream_t s) {
 
 // Binds a routing to the plan, in capture `now`.
 void bind_routing(moe_plan* plan, const int32_t* topk_idx, void* workspace, CaptureId now) {
-  plan->routed = plan->finished = plan->scanned = plan->assigned = false;
+  plan->routed = plan->scanned = plan->assigned = false;
   plan->route_capture = now;
   plan->idx = topk_idx;
   plan->ws = workspace;
@@ -162,8 +162,9 @@ moe_status ensure_assigned(moe_plan* plan, hipStream_t s) {
   if (holds(plan, plan->assigned, plan->assign_capture, now)) return MOE_OK;
   st = scan_in(plan, now, s);
   if (st != MOE_OK) return st;
-  // Recorded for a routing that has run: the ids of the latest route.
-  const int32_t* idx = now != 0 && plan->route_capture == 0 ? nullptr : plan->idx;
+  // Where the route was not recorded together with this, another one of the
+  // plan may come between: the ids of the latest that ran.
+  const int32_t* idx = now == plan->route_capture ? plan->idx : nullptr;
   if (launch_route_assign(plan->d, idx, plan->work, s) != hipSuccess) return MOE_ERR_HIP;
   plan->assigned = true;
   plan->assign_capture = now;
@@ -281,7 +282,7 @@ moe_status moe_plan_create(const moe_config* cfg, moe_plan** out) {
   p->layout = moe::make_layout(d);
   p->idx = nullptr;
   p->ws = nullptr;
-  p->routed = p->finished = p->scanned = p->assigned = false;
+  p->routed = p->scanned = p->assigned = false;
   p->route_capture = p->scan_capture = p->assign_capture = 0;
   p->timer = nullptr;
   *out = p;
@@ -435,7 +436,7 @@ moe_status moe_pipeline(moe_plan* plan, const int32_t* topk_idx, void* workspace
   if (moe::launch_pipeline(plan->d, topk_idx, x, recv, topk_w, out, out_dtype == MOE_OUT_F32,
                            plan->work, s) != hipSuccess)
     return MOE_ERR_HIP;
-  plan->routed = plan->finished = plan->scanned = plan->assigned = true;
+  plan->routed = plan->scanned = plan->assigned = true;
   plan->scan_capture = plan->assign_capture = now;
   return MOE_OK;
 }

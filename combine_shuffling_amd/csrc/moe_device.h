@@ -68,8 +68,8 @@ __device__ __forceinline__ void token_slots(const Dims& d, const Work& w,
 }
 
 // Notes in the workspace where the ids of its latest route are, for an assign
-// that was recorded into a graph: the ids of the route it was recorded after
-// may be gone when it is replayed.
+// that was not recorded (or launched) together with its route: other routes on
+// other ids may have come between when it runs.
 __device__ __forceinline__ void note_ids(const Dims& d, const Work& w, const int32_t* idx) {
   *reinterpret_cast<const int32_t**>(w.ctrl + kCtrlIdx) = idx;
   w.ctrl[kCtrlSlots] = d.T * d.k;

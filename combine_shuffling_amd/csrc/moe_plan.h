@@ -28,7 +28,6 @@ struct moe_plan {
   void* ws;
   moe::Work work;
   bool routed;     // route_count has been launched for the bound routing
-  bool finished;   // by a launch that scans and assigns too (moe_pipeline)
   bool scanned;    // route_scan has been launched for it (tile bases, offsets, status)
   bool assigned;   // slot_of / row_src (and stage_of / stage_src) are final
   // The stream captures that recorded these (0: none, they were launched).
@@ -60,7 +59,7 @@ moe_status capture_of(hipStream_t s, CaptureId* id);
 // capture on a plan that was routed outside of it records its own, so that a
 // graph replayed after another route of the plan computes with that route.
 // And where the route itself was recorded, every replay routes anew, so that
-// each call outside of the graph does them again.
+// each call outside of the graph does again what the graph does not hold.
 //
 // Launches the plan's scan if the route left it to the gather (small plans).
 moe_status ensure_scanned(moe_plan* plan, hipStream_t s);

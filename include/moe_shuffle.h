@@ -58,11 +58,14 @@
  * a plan that was routed outside of the capture records what it needs of the
  * plan (scan, slot arrays) with it, so that a graph replayed after another
  * moe_route_plan of the plan, on the same workspace, computes with that
- * routing; and on a plan whose route was recorded, a call outside of the graph
- * takes the routing of its last replay, of which there has to be one.  Like
- * every other argument, the topk_idx of the route is baked into a recorded
- * moe_dispatch or moe_dispatch_fp8: routes between the replays of those put
- * their ids into the same buffer.
+ * routing; and on a plan whose latest moe_route_plan call was recorded, a call
+ * outside of the graph takes the routing of its last replay, of which there
+ * has to be one.  After a moe_route_plan that is not recorded, a replay of a
+ * route recorded earlier modifies the workspace under it: calls outside of the
+ * graph need a route of their own again.  Like every other argument, the
+ * topk_idx of the route is baked into a recorded moe_dispatch or
+ * moe_dispatch_fp8: routes between the replays of those put their ids into the
+ * same buffer.
  *
  * Bands.  With band_tokens = B > 0 and B < T the batch is cut into
  * nb = ceil(T / B) bands; band b holds tokens [b*B, min((b+1)*B, T)) and owns

@@ -161,6 +161,55 @@ def test_captured_route(name, T, kw, inside, dev):
         c.check(c.all(p), 1, "eager, after a route")
 
 
+@pytest.mark.parametrize("name,T,kw", PLANS, ids=[p[0] for p in PLANS])
+def test_graphs_that_share_a_plan(name, T, kw, dev):
+    # Two graphs that route one plan on ids of their own, and one with the calls alone, recorded
+    # after them.
+    say(f"[graphs] three graphs of one plan, {name}")
+    c = Calls(T, kw, dev)
+    p = c.routed(c.routes[0])
+    routes = [captured(lambda r=r: p.route(r))[0] for r in c.routes]
+    alone, outs = captured(lambda: c.all(p))
+    for n, i in enumerate((1, 0, 0, 1, 0, 1, 0)):
+        if n < 5:
+            routes[i].replay()
+        else:
+            p.route(c.routes[i])      # eager ones
+        for t in outs.values():
+            t.zero_()
+        if n % 2:
+            c.check(c.all(p), i, "eager")
+        alone.replay()
+        torch.cuda.synchronize()
+        c.check(outs, i, "replayed")
+        c.check(c.all(p), i, "eager")
+
+
+@pytest.mark.parametrize("name,T,kw", PLANS, ids=[p[0] for p in PLANS])
+def test_what_a_graph_did_is_not_done_again(name, T, kw, dev):
+    c = Calls(T, kw, dev)
+    p = c.routed(c.routes[0])
+
+    def launched(call):
+        p.timing(16)
+        call()
+        names = [n for n, _, _ in p.timing_read()]
+        p.timing(0)
+        return names
+
+    combine = lambda: p.combine(c.rows, c.w)  # noqa: E731
+    graph, _ = captured(lambda: p.route(c.routes[0]).dispatch(c.x))
+    graph.replay()
+    for _ in range(2):       # the graph holds the route and the dispatch, which assigns
+        assert launched(combine) == ["combine_kernel"]
+    c.check(c.all(p, ("out",)), 0, "after the replay")
+    p.route(c.routes[1])
+    p.dispatch(c.x)
+    for _ in range(2):
+        assert launched(combine) == ["combine_kernel"]
+    c.check(c.all(p, ("out",)), 1, "eager")
+
+
 @pytest.mark.parametrize("band", [0, 256])
 def test_captured_pipeline(band, dev):
     # A pipeline routes and finishes its plan in its own launch, recorded or not.
