@@ -1,7 +1,7 @@
 """MI355X (gfx950) MoE expert-parallel shuffle.
 
-A thin binding over the C ABI of ``libmoeshuffle.so`` (include/moe_shuffle.h and
-include/moe_layer.h): the same calls, with torch tensors for device memory and torch's current
+A thin binding over the C ABI of ``libmoeshuffle.so`` (include/moe_shuffle.h,
+include/moe_layer.h and include/moe_block.h): the same calls, with torch tensors for device memory and torch's current
 stream.  Every step of the shuffle runs in the library's HIP kernels; this
 module only checks shapes and passes pointers.
 
@@ -47,7 +47,8 @@ from ._abi import MoeError, ITEM  # noqa: F401
 
 __all__ = ["Plan", "MoeError", "expert_partition", "route_plan", "dispatch", "combine",
            "dispatch_fp8", "combine_fp8", "combine_hier", "pipeline", "router", "router_backward",
-           "expert_linear", "expert_linear_backward", "combine_backward", "dispatch_backward"]
+           "expert_linear", "expert_linear_backward", "combine_backward", "dispatch_backward", "norm",
+           "norm_backward"]
 
 
 def expert_partition(num_experts: int, num_ranks: int) -> list[int]:
@@ -100,6 +101,14 @@ def _out(t: torch.Tensor | None, shape, dtype, name: str, device) -> torch.Tenso
         stride = (shape[1], 1) if len(shape) == 2 else (shape[1] * shape[2], shape[2], 1)
         return torch.empty_strided(shape, stride, dtype=dtype, device=device)
     _need(t, shape, (dtype,), name, device)
+    return t
+
+
+def _vector(t: torch.Tensor | None, n: int, name: str, device) -> torch.Tensor:
+    """The caller's float32 output [n], checked, or a new one."""
+    if t is None:
+        return torch.empty_strided((n,), (1,), dtype=torch.float32, device=device)
+    _need(t, (n,), _F32, name, device)
     return t
 
 
@@ -558,6 +567,94 @@ class Plan:
                      workspace.data_ptr())
         return grad_x, grad_w, grad_bias
 
+    # -- moe_norm
+    def _norm_config(self, kind: str, eps: float, x: torch.Tensor, y_code: int):
+        if kind not in _abi.NORM:
+            raise ValueError(f"kind must be one of {tuple(_abi.NORM)}")
+        return ctypes.byref(_abi.NormConfig(_abi.NORM[kind], eps, _OUT_CODE[x.dtype], y_code))
+
+    @_on_stream
+    def norm(self, x: torch.Tensor, gamma: torch.Tensor | None = None,
+             beta: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+             kind: str = "layer", eps: float = 1e-5, out_dtype: torch.dtype = torch.bfloat16,
+             save_stats: bool = False, y: torch.Tensor | None = None,
+             total: torch.Tensor | None = None, stats: torch.Tensor | None = None):
+        """Norm of the residual stream's rows: returns (y, total, stats).
+
+        total = x + residual, rounded to x's dtype (None without a residual: x is what is normed);
+        y = (total - mean) * rstd * gamma + beta, [T, H] of out_dtype; kind: "layer", or "rms" for
+        mean = 0.  x, residual: [T, H] float32 or bf16, of one dtype; gamma, beta: [H] float32 (None:
+        ones, zeros).  stats: [T, 2] float32 (mean, rstd) for the gradient, with save_stats (or a
+        tensor to write), else None.  The plan need not be routed."""
+        dev = x.device
+        _need(x, (self.T, self.H), (torch.float32, torch.bfloat16), "x", dev)
+        for t, name in ((gamma, "gamma"), (beta, "beta")):
+            if t is not None:
+                _need(t, (self.H,), _F32, name, dev)
+        if residual is not None:
+            _need(residual, (self.T, self.H), (x.dtype,), "residual", dev)
+        elif total is not None:
+            raise ValueError("total is written with a residual only")
+        cfg = self._norm_config(kind, eps, x, _out_code(out_dtype, "out_dtype"))
+        if y is not None or total is not None or stats is not None:
+            _apart((y, total, stats), (x, gamma, beta, residual))
+        y = _out(y, (self.T, self.H), out_dtype, "y", dev)
+        if residual is not None:
+            total = _out(total, (self.T, self.H), x.dtype, "total", dev)
+        if save_stats or stats is not None:
+            stats = _out(stats, (self.T, 2), torch.float32, "stats", dev)
+        self._launch("moe_norm", dev, cfg, x.data_ptr(), _addr(residual), _addr(gamma), _addr(beta),
+                     y.data_ptr(), _addr(total), _addr(stats))
+        return y, total, stats
+
+    # -- moe_norm_backward
+    @_on_stream
+    def norm_backward(self, grad_y: torch.Tensor, total: torch.Tensor, stats: torch.Tensor,
+                      gamma: torch.Tensor | None = None, grad_total: torch.Tensor | None = None,
+                      kind: str = "layer", x_grad: bool = True, gamma_grad: bool = True,
+                      beta_grad: bool = True, grad_x: torch.Tensor | None = None,
+                      grad_gamma: torch.Tensor | None = None,
+                      grad_beta: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None):
+        """Gradient of norm: returns (grad_x [T, H] of total's dtype, grad_gamma and grad_beta [H]
+        float32), None for one that is not wanted.
+
+        total: what was normed (norm's second output, or its x without a residual); stats: as norm
+        stored them; grad_y: [T, H] float32 or bf16; grad_total: [T, H] of total's dtype, the
+        gradient that reaches total by other ways, added to grad_x.  grad_x is the gradient of x
+        and of the residual.  x_grad, gamma_grad, beta_grad say which are wanted; grad_x,
+        grad_gamma, grad_beta: tensors to write them to."""
+        dev = total.device
+        _need(total, (self.T, self.H), (torch.float32, torch.bfloat16), "total", dev)
+        _need(grad_y, (self.T, self.H), (torch.float32, torch.bfloat16), "grad_y", dev)
+        _need(stats, (self.T, 2), _F32, "stats", dev)
+        if gamma is not None:
+            _need(gamma, (self.H,), _F32, "gamma", dev)
+        if grad_total is not None:
+            _need(grad_total, (self.T, self.H), (total.dtype,), "grad_total", dev)
+        cfg = self._norm_config(kind, 0.0, total, _OUT_CODE[grad_y.dtype])
+        inputs = (grad_y, total, stats, gamma, grad_total)
+        need = self._lib.moe_norm_backward_workspace_bytes(self._h, cfg)
+        if workspace is not None:
+            _need(workspace, getattr(workspace, "shape", ()), (getattr(workspace, "dtype", None),),
+                  "workspace", dev)
+            if workspace.numel() * workspace.element_size() < need:
+                raise ValueError("workspace too small")
+            _apart((workspace,), inputs)
+        elif need and (gamma_grad or beta_grad):
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        given = tuple(t for t, wanted in ((grad_x, x_grad), (grad_gamma, gamma_grad),
+                                          (grad_beta, beta_grad)) if wanted and t is not None)
+        if given:
+            _apart(given, (*inputs, workspace))
+        grad_x = _out(grad_x, (self.T, self.H), total.dtype, "grad_x", dev) if x_grad else None
+        grad_gamma = _vector(grad_gamma, self.H, "grad_gamma", dev) if gamma_grad else None
+        grad_beta = _vector(grad_beta, self.H, "grad_beta", dev) if beta_grad else None
+        self._launch("moe_norm_backward", dev, cfg, grad_y.data_ptr(), total.data_ptr(),
+                     stats.data_ptr(), _addr(gamma), _addr(grad_total), _addr(grad_x),
+                     _addr(grad_gamma), _addr(grad_beta), _addr(workspace))
+        return grad_x, grad_gamma, grad_beta
+
     # -- moe_plan_timing / moe_plan_timing_read
     def timing(self, capacity: int) -> None:
         """Time each kernel this plan's calls launch (up to `capacity` launches;
@@ -691,3 +788,20 @@ def expert_linear_backward(plan: Plan, grad_y: torch.Tensor, x: torch.Tensor | N
     return plan.expert_linear_backward(grad_y, x, w, pre, activation, bias_grad, x_grad, w_grad,
                                        grad_w_dtype, grad_x, grad_w, grad_bias, workspace,
                                        stream=stream)
+
+
+def norm(plan: Plan, x: torch.Tensor, gamma=None, beta=None, residual=None, kind: str = "layer",
+         eps: float = 1e-5, out_dtype: torch.dtype = torch.bfloat16, save_stats: bool = False, y=None,
+         total=None, stats=None, stream=None):
+    """moe_norm: returns (y [T, H], total [T, H] or None, stats [T, 2] float32 or None)."""
+    return plan.norm(x, gamma, beta, residual, kind, eps, out_dtype, save_stats, y, total, stats,
+                     stream=stream)
+
+
+def norm_backward(plan: Plan, grad_y: torch.Tensor, total: torch.Tensor, stats: torch.Tensor,
+                  gamma=None, grad_total=None, kind: str = "layer", x_grad: bool = True,
+                  gamma_grad: bool = True, beta_grad: bool = True, grad_x=None, grad_gamma=None,
+                  grad_beta=None, workspace=None, stream=None):
+    """moe_norm_backward: returns (grad_x, grad_gamma, grad_beta), None where not wanted."""
+    return plan.norm_backward(grad_y, total, stats, gamma, grad_total, kind, x_grad, gamma_grad,
+                              beta_grad, grad_x, grad_gamma, grad_beta, workspace, stream=stream)

@@ -1,4 +1,5 @@
-"""ctypes declarations of the C ABI in include/moe_shuffle.h and include/moe_layer.h.
+"""ctypes declarations of the C ABI in include/moe_shuffle.h, include/moe_layer.h and
+include/moe_block.h.
 
 Loads the in-tree libmoeshuffle.so and fails loudly when it is missing: there
 is no fallback of any kind.
@@ -37,6 +38,9 @@ ROUTER_KEY = dict(logit=0, score=1)
 ACTIVATION = dict(none=0, relu=1, silu=2, gelu=3, swiglu=4, geglu=5)
 GATED = ("swiglu", "geglu")
 
+# moe_block.h: moe_norm_kind
+NORM = dict(layer=0, rms=1)
+
 # moe_item
 ITEM = dict(status=0, counts=1, expert_offsets=2, rank_offsets=3, slot_of=4, row_src=5,
             num_staged=6, stage_offsets=7, stage_of=8, stage_src=9, send_rows=10,
@@ -74,6 +78,15 @@ class ExpertConfig(ctypes.Structure):
     ]
 
 
+class NormConfig(ctypes.Structure):
+    _fields_ = [
+        ("kind", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("x_dtype", ctypes.c_int32),
+        ("y_dtype", ctypes.c_int32),
+    ]
+
+
 # include/moe_shuffle.h
 EXPORTS = (
     "moe_expert_partition", "moe_plan_create", "moe_plan_destroy", "moe_plan_workspace_bytes",
@@ -90,7 +103,11 @@ LAYER_EXPORTS = (
     "moe_expert_linear", "moe_expert_backward_workspace_bytes", "moe_expert_linear_backward",
 )
 
+# include/moe_block.h
+BLOCK_EXPORTS = ("moe_norm", "moe_norm_backward_workspace_bytes", "moe_norm_backward")
+
 KERNEL_COUNT = 33  # moe_kernel and moe_layer_kernel
+BLOCK_KERNELS = range(64, 67)  # moe_block_kernel
 
 
 class MoeError(RuntimeError):
@@ -170,6 +187,13 @@ def lib() -> ctypes.CDLL:
     L.moe_expert_backward_workspace_bytes.restype = sz
     L.moe_expert_linear_backward.argtypes = [vp, expert, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp]
     L.moe_expert_linear_backward.restype = i32
+    norm = ctypes.POINTER(NormConfig)
+    L.moe_norm.argtypes = [vp, norm, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.moe_norm.restype = i32
+    L.moe_norm_backward_workspace_bytes.argtypes = [vp, norm]
+    L.moe_norm_backward_workspace_bytes.restype = sz
+    L.moe_norm_backward.argtypes = [vp, norm, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.moe_norm_backward.restype = i32
     L.moe_status_str.argtypes = [i32]
     L.moe_status_str.restype = ctypes.c_char_p
     _lib = L

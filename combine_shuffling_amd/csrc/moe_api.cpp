@@ -10,7 +10,7 @@
 #include <new>
 #include <vector>
 
-#include "moe_layer.h"
+#include "moe_block.h"
 #include "moe_plan.h"
 
 namespace moe {
@@ -311,6 +311,10 @@ const char* moe_kernel_name(int32_t kernel) {
       "combine_grad_kernel",  "expert_rows_kernel",     "expert_few_rows_kernel",
       "expert_rows_grad_kernel", "expert_wgrad_kernel", "expert_grads_kernel",
       "expert_act_grad_kernel", "expert_bias_sum_kernel"};
+  static const char* const block_names[MOE_BLOCK_KERNEL_END - MOE_KERNEL_NORM] = {
+      "norm_kernel", "norm_grad_kernel", "norm_sum_kernel"};
+  if (kernel >= MOE_KERNEL_NORM && kernel < MOE_BLOCK_KERNEL_END)
+    return block_names[kernel - MOE_KERNEL_NORM];
   return kernel >= 0 && kernel < MOE_LAYER_KERNEL_END ? names[kernel] : "?";
 }
 
