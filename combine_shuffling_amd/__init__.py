@@ -48,7 +48,7 @@ from ._abi import MoeError, ITEM  # noqa: F401
 __all__ = ["Plan", "MoeError", "expert_partition", "route_plan", "dispatch", "combine",
            "dispatch_fp8", "combine_fp8", "combine_hier", "pipeline", "router", "router_backward",
            "expert_linear", "expert_linear_backward", "combine_backward", "dispatch_backward", "norm",
-           "norm_backward"]
+           "norm_backward", "ExpertWeights4", "pack_experts4", "quantize_experts4", "expert_linear4"]
 
 
 def expert_partition(num_experts: int, num_ranks: int) -> list[int]:
@@ -141,6 +141,89 @@ def _on_stream(method):
         with torch.cuda.stream(stream):
             return method(*args, **kw)
     return call
+
+
+def _run(name: str, device: torch.device, *args) -> None:
+    """The library's `name`, of no plan, on the device's current stream."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on the GPU, not on {device}")
+    with torch.cuda.device(device):
+        _abi.check(getattr(_abi.lib(), name)(*args, _stream_handle(device, None)), name)
+
+
+class ExpertWeights4:
+    """Expert weights [experts, rows, in_features] in 4 bits, packed for expert_linear4: made by
+    pack_experts4 or quantize_experts4.  packed: the buffer (uint8)."""
+
+    def __init__(self, experts: int, rows: int, in_features: int, format: str, group: int,
+                 device: torch.device):
+        if format not in _abi.WEIGHTS4:
+            raise ValueError(f"format must be one of {tuple(_abi.WEIGHTS4)}")
+        self.experts, self.rows, self.in_features = experts, rows, in_features
+        self.format, self.group, self.device = format, group, device
+        self._cfg = _abi.Weights4Config(experts, rows, in_features, _abi.WEIGHTS4[format], group)
+        self.cfg = ctypes.byref(self._cfg)
+        size = _abi.lib().moe_weights4_bytes(self.cfg)
+        if size == 0:
+            raise ValueError(f"{format} weights of {experts} x {rows} x {in_features} in groups of "
+                             f"{group} are not supported")
+        self.packed = torch.empty(size, dtype=torch.uint8, device=device)
+
+    def values(self, dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
+        """moe_weights4_unpack: the values that the weights stand for, [experts, rows,
+        in_features] of dtype (float32 or bf16)."""
+        if stream is not None and stream.device != self.device:
+            raise ValueError(f"stream is on {stream.device}, the weights on {self.device}")
+        return _values4(self, dtype, stream=stream)
+
+
+@_on_stream
+def _values4(w4: ExpertWeights4, dtype: torch.dtype) -> torch.Tensor:
+    code = _out_code(dtype, "dtype")
+    w = torch.empty((w4.experts, w4.rows, w4.in_features), dtype=dtype, device=w4.device)
+    _run("moe_weights4_unpack", w4.device, w4.cfg,
+         w4.packed.data_ptr(), w.data_ptr(), code)
+    return w
+
+
+@_on_stream
+def pack_experts4(codes: torch.Tensor, scales: torch.Tensor, format: str = "int4",
+                  group: int = 128) -> ExpertWeights4:
+    """moe_weights4_pack: codes [experts, rows, in / 2] uint8 (weight 2j in the lower nibble of byte
+    j) and scales [experts, rows, ceil(in / group)] as a checkpoint holds them -> packed weights.
+
+    format "int4": scale * (code - 8), bf16 scales, groups of 32, 64 or 128; "e2m1": 2^(scale - 127)
+    times the OCP E2M1 value, uint8 (E8M0) scales, groups of 32."""
+    if not isinstance(codes, torch.Tensor):
+        raise TypeError("codes must be a torch.Tensor")
+    if codes.dim() != 3:
+        raise ValueError(f"codes has shape {tuple(codes.shape)}, expected [experts, rows, in / 2]")
+    dev = codes.device
+    E, Z, K = codes.shape[0], codes.shape[1], codes.shape[2] * 2
+    _need(codes, (E, Z, K // 2), (torch.uint8,), "codes", dev)
+    w4 = ExpertWeights4(E, Z, K, format, group, dev)
+    kinds = (torch.bfloat16,) if format == "int4" else (torch.uint8,)
+    _need(scales, (E, Z, -(-K // group)), kinds, "scales", dev)
+    _run("moe_weights4_pack", dev, w4.cfg, codes.data_ptr(),
+         scales.data_ptr(), w4.packed.data_ptr())
+    return w4
+
+
+@_on_stream
+def quantize_experts4(w: torch.Tensor, format: str = "int4", group: int = 128) -> ExpertWeights4:
+    """moe_weights4_quantize: bf16 weights [experts, rows, in] -> packed weights.
+
+    "int4": scale = max |w| / 7 of the group, rounded to bf16; "e2m1" (group 32): the smallest power
+    of two with max |w| <= 6 * scale.  Codes are rounded to nearest even."""
+    if not isinstance(w, torch.Tensor):
+        raise TypeError("w must be a torch.Tensor")
+    if w.dim() != 3:
+        raise ValueError(f"w has shape {tuple(w.shape)}, expected [experts, rows, in]")
+    _need(w, tuple(w.shape), _BF16, "w", w.device)
+    w4 = ExpertWeights4(*w.shape, format, group, w.device)
+    _run("moe_weights4_quantize", w.device, w4.cfg, w.data_ptr(),
+         w4.packed.data_ptr())
+    return w4
 
 
 class Plan:
@@ -567,6 +650,46 @@ class Plan:
                      workspace.data_ptr())
         return grad_x, grad_w, grad_bias
 
+    # -- moe_expert_linear4
+    @_on_stream
+    def expert_linear4(self, x: torch.Tensor, w4: ExpertWeights4, bias: torch.Tensor | None = None,
+                       residual: torch.Tensor | None = None, activation: str = "none",
+                       y: torch.Tensor | None = None) -> torch.Tensor:
+        """expert_linear with 4-bit weights, for serving (no gradient): returns y [T*k, N] bf16.
+
+        w4: what pack_experts4 or quantize_experts4 made of weights [E, Z, K]; Z = 2N (gate rows,
+        then up rows) with "swiglu" and "geglu", else N.  x [T*k, K], residual [T*k, N] bf16, bias
+        [E, Z] float32."""
+        dev = self.device
+        if dev is None:
+            raise MoeError(_abi.ERR_PLAN_NOT_ROUTED, "expert_linear4")
+        if activation not in _abi.ACTIVATION:
+            raise ValueError(f"activation must be one of {tuple(_abi.ACTIVATION)}")
+        if not isinstance(w4, ExpertWeights4):
+            raise TypeError("w4 must be ExpertWeights4")
+        if w4.experts != self.E:
+            raise ValueError(f"w4 has {w4.experts} experts, expected {self.E}")
+        K, Z = w4.in_features, w4.rows
+        N = Z
+        if activation in _abi.GATED:
+            if Z % 16:
+                raise ValueError("a gated activation needs halves of a multiple of 8 weight rows")
+            N = Z // 2
+        rows = self.recv_rows
+        _need(w4.packed, w4.packed.shape, (torch.uint8,), "w4", dev)
+        _need(x, (rows, K), _BF16, "x", dev)
+        if bias is not None:
+            _need(bias, (self.E, Z), _F32, "bias", dev)
+        if residual is not None:
+            _need(residual, (rows, N), _BF16, "residual", dev)
+        if y is not None:
+            _apart((y,), (x, w4.packed, bias, residual))
+        y = _out(y, (rows, N), torch.bfloat16, "y", dev)
+        cfg = ctypes.byref(_abi.ExpertConfig(K, N, _abi.ACTIVATION[activation]))
+        self._launch("moe_expert_linear4", dev, cfg, w4.cfg, x.data_ptr(), w4.packed.data_ptr(),
+                     _addr(bias), _addr(residual), y.data_ptr())
+        return y
+
     # -- moe_norm
     def _norm_config(self, kind: str, eps: float, x: torch.Tensor, y_code: int):
         if kind not in _abi.NORM:
@@ -788,6 +911,12 @@ def expert_linear_backward(plan: Plan, grad_y: torch.Tensor, x: torch.Tensor | N
     return plan.expert_linear_backward(grad_y, x, w, pre, activation, bias_grad, x_grad, w_grad,
                                        grad_w_dtype, grad_x, grad_w, grad_bias, workspace,
                                        stream=stream)
+
+
+def expert_linear4(plan: Plan, x: torch.Tensor, w4: ExpertWeights4, bias=None, residual=None,
+                   activation: str = "none", y=None, stream=None) -> torch.Tensor:
+    """moe_expert_linear4: returns y [T*k, N] bf16."""
+    return plan.expert_linear4(x, w4, bias, residual, activation, y, stream=stream)
 
 
 def norm(plan: Plan, x: torch.Tensor, gamma=None, beta=None, residual=None, kind: str = "layer",

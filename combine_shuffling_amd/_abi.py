@@ -38,8 +38,9 @@ ROUTER_KEY = dict(logit=0, score=1)
 ACTIVATION = dict(none=0, relu=1, silu=2, gelu=3, swiglu=4, geglu=5)
 GATED = ("swiglu", "geglu")
 
-# moe_block.h: moe_norm_kind
+# moe_block.h: moe_norm_kind, moe_weights4_format
 NORM = dict(layer=0, rms=1)
+WEIGHTS4 = dict(int4=0, e2m1=1)
 
 # moe_item
 ITEM = dict(status=0, counts=1, expert_offsets=2, rank_offsets=3, slot_of=4, row_src=5,
@@ -87,6 +88,16 @@ class NormConfig(ctypes.Structure):
     ]
 
 
+class Weights4Config(ctypes.Structure):
+    _fields_ = [
+        ("experts", ctypes.c_int32),
+        ("rows", ctypes.c_int32),
+        ("in_features", ctypes.c_int32),
+        ("format", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+    ]
+
+
 # include/moe_shuffle.h
 EXPORTS = (
     "moe_expert_partition", "moe_plan_create", "moe_plan_destroy", "moe_plan_workspace_bytes",
@@ -104,10 +115,13 @@ LAYER_EXPORTS = (
 )
 
 # include/moe_block.h
-BLOCK_EXPORTS = ("moe_norm", "moe_norm_backward_workspace_bytes", "moe_norm_backward")
+BLOCK_EXPORTS = (
+    "moe_norm", "moe_norm_backward_workspace_bytes", "moe_norm_backward", "moe_weights4_bytes",
+    "moe_weights4_pack", "moe_weights4_quantize", "moe_weights4_unpack", "moe_expert_linear4",
+)
 
 KERNEL_COUNT = 33  # moe_kernel and moe_layer_kernel
-BLOCK_KERNELS = range(64, 67)  # moe_block_kernel
+BLOCK_KERNELS = range(64, 68)  # moe_block_kernel
 
 
 class MoeError(RuntimeError):
@@ -194,6 +208,17 @@ def lib() -> ctypes.CDLL:
     L.moe_norm_backward_workspace_bytes.restype = sz
     L.moe_norm_backward.argtypes = [vp, norm, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.moe_norm_backward.restype = i32
+    w4 = ctypes.POINTER(Weights4Config)
+    L.moe_weights4_bytes.argtypes = [w4]
+    L.moe_weights4_bytes.restype = sz
+    L.moe_weights4_pack.argtypes = [w4, vp, vp, vp, vp]
+    L.moe_weights4_pack.restype = i32
+    L.moe_weights4_quantize.argtypes = [w4, vp, vp, vp]
+    L.moe_weights4_quantize.restype = i32
+    L.moe_weights4_unpack.argtypes = [w4, vp, vp, i32, vp]
+    L.moe_weights4_unpack.restype = i32
+    L.moe_expert_linear4.argtypes = [vp, expert, w4, vp, vp, vp, vp, vp, vp]
+    L.moe_expert_linear4.restype = i32
     L.moe_status_str.argtypes = [i32]
     L.moe_status_str.restype = ctypes.c_char_p
     _lib = L

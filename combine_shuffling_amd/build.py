@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmoeshuffle.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ("route_plan.hip", "move.hip", "pipeline.hip", "router.hip", "shuffle_grad.hip", "expert.hip",
-           "norm.hip", "moe_api.cpp", "moe_layer_api.cpp", "moe_block_api.cpp")
+           "norm.hip", "weights4.hip", "moe_api.cpp", "moe_layer_api.cpp", "moe_block_api.cpp")
 
 # -packed-fp32-ops: no packed fp32 instructions in device code.
 HIP_FLAGS = [

@@ -51,13 +51,15 @@
 // contiguous contraction are sent past the descriptor's end, so that they
 // read as zeros on both sides (0 * NaN would not be 0).
 #include <algorithm>
+#include <type_traits>
 
-#include "layer_internal.h"
+#include "block_internal.h"
 
 namespace moe {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -1366,3 +1368,5 @@ hipError_t launch_expert_bias_sum(const ExpertDims& x, const int32_t* off, const
 }
 
 }  // namespace moe
+
+#include "expert4.h"

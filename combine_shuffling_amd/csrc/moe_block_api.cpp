@@ -31,6 +31,24 @@ size_t norm_workspace(const NormDims& n) {
   return p > 1 ? ((size_t)2 * p * n.H * sizeof(float) + 255) / 256 * 256 : 0;
 }
 
+constexpr int32_t kMaxFeatures = 1 << 20;
+constexpr int64_t kMaxWeight = (int64_t)1 << 30;  // elements of one expert's weight
+
+moe_status weights4(const moe_weights4_config* c, Weights4* out) {
+  if (!c) return MOE_ERR_INVALID_ARGUMENT;
+  if (c->experts <= 0 || c->rows <= 0 || c->rows % 8 || c->in_features <= 0 || c->in_features % 8)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (c->format != MOE_W4_INT4 && c->format != MOE_W4_E2M1) return MOE_ERR_INVALID_ARGUMENT;
+  const bool e2m1 = c->format == MOE_W4_E2M1;
+  if (c->group != 32 && (e2m1 || (c->group != 64 && c->group != 128)))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (c->experts > MOE_MAX_EXPERTS || c->rows > kMaxFeatures || c->in_features > kMaxFeatures ||
+      (int64_t)c->rows * c->in_features >= kMaxWeight)
+    return MOE_ERR_UNSUPPORTED;
+  *out = Weights4{c->experts, c->rows, c->in_features, e2m1, c->group, (c->in_features + 127) / 128};
+  return MOE_OK;
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -78,6 +96,70 @@ moe_status moe_norm_backward(moe_plan* plan, const moe_norm_config* cfg, const v
   return moe::from_hip(moe::launch_norm_grad(n, grad_y, total, stats, gamma, grad_total, grad_x,
                                              grad_gamma, grad_beta, static_cast<float*>(workspace),
                                              static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_weights4_bytes(const moe_weights4_config* cfg) {
+  moe::Weights4 w;
+  return moe::weights4(cfg, &w) == MOE_OK ? (size_t)(w.codes_bytes() + w.scales_bytes()) : 0;
+}
+
+moe_status moe_weights4_pack(const moe_weights4_config* cfg, const uint8_t* codes,
+                             const void* scales, void* packed, void* stream) {
+  moe::Weights4 w;
+  const moe_status ok = moe::weights4(cfg, &w);
+  if (ok != MOE_OK) return ok;
+  if (!moe::good(codes, 16) || !moe::good(scales, w.e2m1 ? 1 : 2) || !moe::good(packed, 256))
+    return MOE_ERR_INVALID_ARGUMENT;
+  return moe::from_hip(moe::launch_pack4(w, codes, scales, packed, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_weights4_quantize(const moe_weights4_config* cfg, const uint16_t* from, void* packed,
+                                 void* stream) {
+  moe::Weights4 w;
+  const moe_status ok = moe::weights4(cfg, &w);
+  if (ok != MOE_OK) return ok;
+  if (!moe::good(from, 16) || !moe::good(packed, 256)) return MOE_ERR_INVALID_ARGUMENT;
+  return moe::from_hip(moe::launch_quantize4(w, from, packed, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_weights4_unpack(const moe_weights4_config* cfg, const void* packed, void* to,
+                               int32_t w_dtype, void* stream) {
+  moe::Weights4 w;
+  const moe_status ok = moe::weights4(cfg, &w);
+  if (ok != MOE_OK) return ok;
+  if (!moe::is_dtype(w_dtype)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!moe::good(packed, 256) || !moe::good(to, 16)) return MOE_ERR_INVALID_ARGUMENT;
+  return moe::from_hip(moe::launch_unpack4(w, packed, to, w_dtype == MOE_OUT_F32,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_expert_linear4(moe_plan* plan, const moe_expert_config* cfg,
+                              const moe_weights4_config* w4, const uint16_t* x, const void* packed,
+                              const float* bias, const uint16_t* residual, uint16_t* y,
+                              void* stream) {
+  if (!plan || !cfg) return MOE_ERR_INVALID_ARGUMENT;
+  moe::Weights4 w;
+  const moe_status ok = moe::weights4(w4, &w);
+  if (ok != MOE_OK) return ok;
+  if (cfg->activation < MOE_ACT_NONE || cfg->activation > MOE_ACT_GEGLU || cfg->out_features <= 0 ||
+      cfg->out_features % 8)
+    return MOE_ERR_INVALID_ARGUMENT;
+  const moe::Dims& d = plan->d;
+  const int64_t Z = (int64_t)cfg->out_features * (moe::gated(cfg->activation) ? 2 : 1);
+  if (w.E != d.E || w.Z != Z || w.K != cfg->in_features) return MOE_ERR_INVALID_ARGUMENT;
+  const moe::TimerScope timing(plan);
+  if (!plan->routed) return MOE_ERR_PLAN_NOT_ROUTED;
+  if (d.T == 0) return MOE_OK;
+  if (!moe::good(x, 16) || !moe::good(packed, 256) || !moe::aligned(bias, 16) ||
+      !moe::aligned(residual, 16) || !moe::good(y, 16))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const moe::ExpertDims dims{d.T * d.k, d.E,            w.K,      cfg->out_features, (int32_t)Z,
+                             d.T,       cfg->activation, d.nbands, d.band};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const moe_status st = moe::ensure_scanned(plan, s);
+  if (st != MOE_OK) return st;
+  return moe::from_hip(moe::launch_expert_rows4(dims, w, plan->work.expert_off, x, packed, bias,
+                                                residual, y, s));
 }
 
 }  // extern "C"

@@ -83,12 +83,72 @@ moe_status moe_norm_backward(moe_plan* plan, const moe_norm_config* cfg, const v
                              const void* grad_total, void* grad_x, float* grad_gamma,
                              float* grad_beta, void* workspace, void* stream);
 
+/* ---- the experts' products with 4-bit weights -------------------------------- */
+
+typedef enum moe_weights4_format {
+  MOE_W4_INT4 = 0, /* w = scale * (code - 8), scale bf16, a scale per group of 32, 64 or 128    */
+  MOE_W4_E2M1 = 1  /* w = 2^(scale - 127) * OCP E2M1 value (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+                      negatives), scale E8M0 (255: NaN), a scale per group of 32              */
+} moe_weights4_format;
+
+typedef struct moe_weights4_config {
+  int32_t experts;     /* E > 0                                                      */
+  int32_t rows;        /* Z > 0, multiple of 8: weight rows an expert                */
+  int32_t in_features; /* K > 0, multiple of 8                                       */
+  int32_t format;      /* moe_weights4_format                                        */
+  int32_t group;       /* weights of a row that share a scale; a row's last group may have fewer */
+} moe_weights4_config;
+
+/* Packed weights: codes in the order in which the matrix cores take them, and
+ * scales, in one device buffer of moe_weights4_bytes (a multiple of 256; 0 for
+ * a cfg that the calls refuse), 256-byte aligned.  The layout is the library's
+ * own.
+ * Limits of these calls: E <= MOE_MAX_EXPERTS, Z * K < 2^30, K and Z <= 2^20.
+ * Errors of all of them: INVALID_ARGUMENT, UNSUPPORTED (sizes beyond the
+ * limits), HIP. */
+size_t moe_weights4_bytes(const moe_weights4_config* cfg);
+
+/* Packs codes as a checkpoint holds them.  codes: [E, Z, K / 2] uint8, weight
+ * 2j in the lower nibble of byte j; scales: [E, Z, ceil(K / group)] bf16
+ * (INT4, any value) or uint8 (E2M1). */
+moe_status moe_weights4_pack(const moe_weights4_config* cfg, const uint8_t* codes,
+                             const void* scales, void* packed, void* stream);
+
+/* Quantizes bf16 weights w [E, Z, K].  INT4: scale = max |w| / 7 over the group,
+ * rounded to bf16; code - 8 = w / scale rounded to nearest even, within -8 and
+ * 7.  E2M1: scale = the smallest power of two with max |w| <= 6 * scale (within
+ * E8M0's range; 1 for a group of zeros); code = w / scale rounded to nearest
+ * (ties to the even code).  A group that holds an infinity or a NaN gets the
+ * scale NaN. */
+moe_status moe_weights4_quantize(const moe_weights4_config* cfg, const uint16_t* w, void* packed,
+                                 void* stream);
+
+/* The values that packed weights stand for: w [E, Z, K] of w_dtype
+ * (moe_out_dtype; scale * code is rounded once, to it). */
+moe_status moe_weights4_unpack(const moe_weights4_config* cfg, const void* packed, void* w,
+                               int32_t w_dtype, void* stream);
+
+/* Expert product with packed weights, for serving (it has no gradient): for
+ * every receive row r of expert e,
+ *   z[r] = x[r] . w[e]^T + bias[e]        (float32 accumulation)
+ *   y[r] = act(z[r]) + residual[r]        rounded to bf16 (nearest even)
+ * Arguments as moe_expert_linear; w4->experts, rows and in_features are the
+ * plan's E and cfg's Z and K.  A row of x with an infinity or a NaN gives a
+ * row that is not finite.
+ * Errors: PLAN_NOT_ROUTED, INVALID_ARGUMENT, UNSUPPORTED (sizes beyond the
+ * limits), HIP. */
+moe_status moe_expert_linear4(moe_plan* plan, const moe_expert_config* cfg,
+                              const moe_weights4_config* w4, const uint16_t* x, const void* packed,
+                              const float* bias, const uint16_t* residual, uint16_t* y,
+                              void* stream);
+
 /* Kernels of these calls, as moe_plan_timing_read names them (moe_kernel_name
  * takes their ids too). */
 typedef enum moe_block_kernel {
   MOE_KERNEL_NORM = 64,
   MOE_KERNEL_NORM_GRAD,
-  MOE_KERNEL_NORM_SUM,         /* partial sums of the weights' gradients added up */
+  MOE_KERNEL_NORM_SUM,         /* partial sums of the weights' gradients added up  */
+  MOE_KERNEL_EXPERT4_FEW_ROWS, /* product with 4-bit weights, few rows an expert   */
   MOE_BLOCK_KERNEL_END
 } moe_block_kernel;
 

@@ -188,3 +188,141 @@ def test_norm_gradient_definition_against_differences():
                 want[at] = (f(*up) - f(*down)) / 2e-5
             # differences: third derivatives times 1e-10, and 2^-52 of sums of 72 terms over 1e-5
             assert np.abs(got[name][0] - want).max() < 1e-6, (rms, name)
+
+
+# ---- 4-bit weights
+
+def w4cfg(E=8, Z=64, K=64, fmt=0, group=128):
+    return _abi.Weights4Config(E, Z, K, fmt, group)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(E=0), BAD), (dict(E=-1), BAD), (dict(Z=0), BAD), (dict(Z=12), BAD), (dict(K=0), BAD),
+    (dict(K=-8), BAD), (dict(K=60), BAD), (dict(fmt=2), BAD), (dict(fmt=-1), BAD), (dict(group=0), BAD),
+    (dict(group=16), BAD), (dict(group=96), BAD), (dict(group=256), BAD), (dict(group=-32), BAD),
+    (dict(fmt=1, group=64), BAD), (dict(fmt=1, group=128), BAD),
+    (dict(E=1025), UNSUPPORTED), (dict(K=(1 << 20) + 8), UNSUPPORTED), (dict(Z=(1 << 20) + 8), UNSUPPORTED),
+    (dict(Z=1 << 15, K=1 << 15), UNSUPPORTED),
+])
+def test_weights4_config_refusals(kw, want):
+    L, c = _abi.lib(), ctypes.byref(w4cfg(**kw))
+    assert L.moe_weights4_bytes(c) == 0
+    assert L.moe_weights4_pack(c, vp(256), vp(256), vp(256), None) == want
+    assert L.moe_weights4_quantize(c, vp(256), vp(256), None) == want
+    assert L.moe_weights4_unpack(c, vp(256), vp(256), 0, None) == want
+    e = _abi.ExpertConfig(64, 64, 0)
+    assert L.moe_expert_linear4(plan()._h, ctypes.byref(e), c, vp(256), vp(256), None, None, vp(256),
+                                None) == want
+
+
+def test_weights4_pointer_refusals():
+    L, c = _abi.lib(), ctypes.byref(w4cfg())
+    m = ctypes.byref(w4cfg(fmt=1, group=32))
+    assert L.moe_weights4_pack(None, vp(256), vp(256), vp(256), None) == BAD
+    for codes, scales, packed in ((None, 256, 256), (8, 256, 256), (256, None, 256), (256, 257, 256),
+                                  (256, 256, None), (256, 256, 128)):
+        assert L.moe_weights4_pack(c, vp(codes), vp(scales), vp(packed), None) == BAD
+    assert L.moe_weights4_pack(m, vp(256), None, vp(256), None) == BAD
+    for w, packed in ((None, 256), (8, 256), (256, None), (256, 16)):
+        assert L.moe_weights4_quantize(c, vp(w), vp(packed), None) == BAD
+        assert L.moe_weights4_unpack(c, vp(packed), vp(w), 0, None) == BAD
+    assert L.moe_weights4_unpack(c, vp(256), vp(256), 2, None) == BAD
+    assert L.moe_weights4_bytes(None) == 0
+
+
+def test_weights4_bytes():
+    size = lambda **kw: _abi.lib().moe_weights4_bytes(ctypes.byref(w4cfg(**kw)))  # noqa: E731
+    # blocks of 128 weights of a row in 64 bytes, and their scales
+    assert size(E=2, Z=64, K=256) == 2 * 64 * 128 + 2 * 64 * 2 * 2
+    assert size(E=2, Z=64, K=256, group=32) == 2 * 64 * 128 + 2 * 64 * 8 * 2
+    assert size(E=2, Z=64, K=256, fmt=1, group=32) == 2 * 64 * 128 + 2 * 64 * 8
+    assert size(E=2, Z=64, K=136) == size(E=2, Z=64, K=256)
+    assert size(E=1, Z=8, K=8) == 512 + 256
+
+
+def test_expert_linear4_refusals():
+    L, p = _abi.lib(), plan()
+
+    def call(cfg=(64, 64, 0), w4=None, x=16, packed=256, bias=None, residual=None, y=16, plan_=p._h):
+        c = ctypes.byref(_abi.ExpertConfig(*cfg)) if cfg else None
+        return L.moe_expert_linear4(plan_, c, ctypes.byref(w4 or w4cfg()), vp(x), vp(packed), vp(bias),
+                                    vp(residual), vp(y), None)
+
+    assert call() == _abi.ERR_PLAN_NOT_ROUTED
+    assert call(plan_=None) == call(cfg=None) == BAD
+    assert L.moe_expert_linear4(p._h, ctypes.byref(_abi.ExpertConfig(64, 64, 0)), None, vp(16), vp(256),
+                                None, None, vp(16), None) == BAD
+    for cfg, w4 in [((64, 64, 6), None), ((64, 64, -1), None), ((64, 0, 0), None), ((64, 12, 0), None),
+                    ((72, 64, 0), None), ((64, 72, 0), None), ((64, 64, 4), None),      # Z = 2N when gated
+                    ((64, 64, 0), w4cfg(E=7)), ((64, 64, 0), w4cfg(Z=128))]:
+        assert call(cfg, w4) == BAD, cfg
+    assert call((64, 32, 4)) == _abi.ERR_PLAN_NOT_ROUTED
+
+
+def test_weights4_binding_refusals():
+    codes = torch.zeros(8, 64, 32, dtype=torch.uint8)
+    bf = torch.zeros(8, 64, 1, dtype=torch.bfloat16)
+    for call, match in [
+        (lambda: cs.pack_experts4(codes, bf, "int8"), "format"),
+        (lambda: cs.pack_experts4(codes[0], bf), "expected"),
+        (lambda: cs.pack_experts4(codes.int(), bf), "codes"),
+        (lambda: cs.pack_experts4(codes[:, :, ::2], bf), "contiguous"),
+        (lambda: cs.pack_experts4(codes, bf, group=0), "not supported"),
+        (lambda: cs.pack_experts4(codes, bf, group=48), "not supported"),
+        (lambda: cs.pack_experts4(codes[:, :, :3].contiguous(), bf), "not supported"),
+        (lambda: cs.pack_experts4(codes, bf, group=32), "scales"),
+        (lambda: cs.pack_experts4(codes, bf.float()), "scales"),
+        (lambda: cs.pack_experts4(codes, torch.zeros(8, 64, 2, dtype=torch.bfloat16), "e2m1", 32), "scales"),
+        (lambda: cs.pack_experts4(codes, bf, "e2m1", 128), "not supported"),
+        (lambda: cs.pack_experts4(codes, bf), "GPU"),
+        (lambda: cs.quantize_experts4(torch.zeros(8, 64, 64)), "dtype"),
+        (lambda: cs.quantize_experts4(torch.zeros(8, 64)), "expected"),
+        (lambda: cs.quantize_experts4(torch.zeros(8, 64, 64, dtype=torch.bfloat16).transpose(1, 2)),
+         "contiguous"),
+        (lambda: cs.quantize_experts4(torch.zeros(8, 64, 64, dtype=torch.bfloat16)), "GPU"),
+    ]:
+        with pytest.raises(ValueError, match=match):
+            call()
+    p = plan()
+    w4 = cs.ExpertWeights4(8, 32, 64, "int4", 128, torch.device("cpu"))
+    with pytest.raises(ValueError, match="GPU"):
+        w4.values()
+    with pytest.raises(ValueError, match="dtype"):
+        w4.values(torch.float16)
+    x = torch.zeros(128, 64, dtype=torch.bfloat16)
+    with pytest.raises(cs.MoeError):       # not routed
+        p.expert_linear4(x, w4)
+    p.device = torch.device("cpu")         # as if routed: the checks come before any launch
+    out = torch.zeros(128, 32, dtype=torch.bfloat16)
+    for call, match in [
+        (lambda: p.expert_linear4(x, w4, activation="tanh"), "activation"),
+        (lambda: p.expert_linear4(x, cs.ExpertWeights4(7, 32, 64, "int4", 128, p.device)), "experts"),
+        (lambda: p.expert_linear4(x, cs.ExpertWeights4(8, 40, 64, "int4", 128, p.device),
+                                  activation="swiglu"), "halves"),
+        (lambda: p.expert_linear4(x[:, :32], w4), "x has"),
+        (lambda: p.expert_linear4(x.float(), w4), "x has"),
+        (lambda: p.expert_linear4(x, w4, bias=torch.zeros(8, 64)), "bias"),
+        (lambda: p.expert_linear4(x, w4, residual=x), "residual"),
+        (lambda: p.expert_linear4(x, w4, y=x.clone()), "y has"),
+        (lambda: p.expert_linear4(x, w4, residual=out, y=out), "shares"),
+        (lambda: p.expert_linear4(x, w4), "GPU"),
+    ]:
+        with pytest.raises(ValueError, match=match):
+            call()
+    with pytest.raises(TypeError):
+        p.expert_linear4(x, torch.zeros(8, 32, 64, dtype=torch.bfloat16))
+
+
+def test_quantizer_definition():
+    # Hand-made groups: codes and scales as the formats' rules give them.
+    w = np.zeros((1, 3, 32))
+    w[0, 0, :4] = [7, -7, 3.5, 0.5]            # scale 1: halves go to the even code
+    w[0, 1, :4] = [-14, 3, 5, 6.9]             # scale 2: 1.5 and 2.5 both go to 2
+    codes, scales = block_ref.quantize4(w, "int4", 32)
+    assert scales[0].tolist() == [[1.0], [2.0], [0.0]]
+    assert codes[0, :, :4].tolist() == [[15, 1, 12, 8], [1, 10, 10, 11], [8] * 4]
+    w[0, 0, :8] = [6, -6, 5, 3.5, 2.5, 0.25, 0.75, -1.25]
+    w[0, 1, :2] = [6.25, 0.1]
+    codes, scales = block_ref.quantize4(w, "e2m1", 32)
+    assert scales[0].tolist() == [[127], [128], [127]]
+    assert codes[0, 0, :8].tolist() == [7, 15, 6, 6, 4, 0, 2, 10]
