@@ -121,7 +121,7 @@ BLOCK_EXPORTS = (
 )
 
 KERNEL_COUNT = 33  # moe_kernel and moe_layer_kernel
-BLOCK_KERNELS = range(64, 68)  # moe_block_kernel
+BLOCK_KERNELS = range(64, 69)  # moe_block_kernel
 
 
 class MoeError(RuntimeError):

@@ -312,7 +312,8 @@ const char* moe_kernel_name(int32_t kernel) {
       "expert_rows_grad_kernel", "expert_wgrad_kernel", "expert_grads_kernel",
       "expert_act_grad_kernel", "expert_bias_sum_kernel"};
   static const char* const block_names[MOE_BLOCK_KERNEL_END - MOE_KERNEL_NORM] = {
-      "norm_kernel", "norm_grad_kernel", "norm_sum_kernel", "expert4_few_rows_kernel"};
+      "norm_kernel", "norm_grad_kernel", "norm_sum_kernel", "expert4_rows_kernel",
+      "expert4_few_rows_kernel"};
   if (kernel >= MOE_KERNEL_NORM && kernel < MOE_BLOCK_KERNEL_END)
     return block_names[kernel - MOE_KERNEL_NORM];
   return kernel >= 0 && kernel < MOE_LAYER_KERNEL_END ? names[kernel] : "?";

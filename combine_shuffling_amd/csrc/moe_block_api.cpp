@@ -45,7 +45,8 @@ moe_status weights4(const moe_weights4_config* c, Weights4* out) {
   if (c->experts > MOE_MAX_EXPERTS || c->rows > kMaxFeatures || c->in_features > kMaxFeatures ||
       (int64_t)c->rows * c->in_features >= kMaxWeight)
     return MOE_ERR_UNSUPPORTED;
-  *out = Weights4{c->experts, c->rows, c->in_features, e2m1, c->group, (c->in_features + 127) / 128};
+  *out = Weights4{c->experts, c->rows,  c->in_features, e2m1,
+                  c->group,   (c->in_features + 127) / 128, (c->rows + 15) / 16};
   return MOE_OK;
 }
 

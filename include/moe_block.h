@@ -86,7 +86,8 @@ moe_status moe_norm_backward(moe_plan* plan, const moe_norm_config* cfg, const v
 /* ---- the experts' products with 4-bit weights -------------------------------- */
 
 typedef enum moe_weights4_format {
-  MOE_W4_INT4 = 0, /* w = scale * (code - 8), scale bf16, a scale per group of 32, 64 or 128    */
+  MOE_W4_INT4 = 0, /* w = scale * (code - 8), scale bf16, below 2^117 in magnitude, a scale per
+                      group of 32, 64 or 128                                                  */
   MOE_W4_E2M1 = 1  /* w = 2^(scale - 127) * OCP E2M1 value (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
                       negatives), scale E8M0 (255: NaN), a scale per group of 32              */
 } moe_weights4_format;
@@ -110,7 +111,7 @@ size_t moe_weights4_bytes(const moe_weights4_config* cfg);
 
 /* Packs codes as a checkpoint holds them.  codes: [E, Z, K / 2] uint8, weight
  * 2j in the lower nibble of byte j; scales: [E, Z, ceil(K / group)] bf16
- * (INT4, any value) or uint8 (E2M1). */
+ * (INT4) or uint8 (E2M1). */
 moe_status moe_weights4_pack(const moe_weights4_config* cfg, const uint8_t* codes,
                              const void* scales, void* packed, void* stream);
 
@@ -132,7 +133,9 @@ moe_status moe_weights4_unpack(const moe_weights4_config* cfg, const void* packe
  * every receive row r of expert e,
  *   z[r] = x[r] . w[e]^T + bias[e]        (float32 accumulation)
  *   y[r] = act(z[r]) + residual[r]        rounded to bf16 (nearest even)
- * Arguments as moe_expert_linear; w4->experts, rows and in_features are the
+ * E2M1 weights are multiplied as they are; so are INT4 weights where experts have
+ * few rows, and where they have many as scale * (code - 8) rounded to bf16, the
+ * type that the matrix cores take.  Arguments as moe_expert_linear; w4->experts, rows and in_features are the
  * plan's E and cfg's Z and K.  A row of x with an infinity or a NaN gives a
  * row that is not finite.
  * Errors: PLAN_NOT_ROUTED, INVALID_ARGUMENT, UNSUPPORTED (sizes beyond the
@@ -148,7 +151,8 @@ typedef enum moe_block_kernel {
   MOE_KERNEL_NORM = 64,
   MOE_KERNEL_NORM_GRAD,
   MOE_KERNEL_NORM_SUM,         /* partial sums of the weights' gradients added up  */
-  MOE_KERNEL_EXPERT4_FEW_ROWS, /* product with 4-bit weights, few rows an expert   */
+  MOE_KERNEL_EXPERT4_ROWS,     /* product with 4-bit weights                       */
+  MOE_KERNEL_EXPERT4_FEW_ROWS, /* the same for batches of few rows an expert       */
   MOE_BLOCK_KERNEL_END
 } moe_block_kernel;
 

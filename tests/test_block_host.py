@@ -237,7 +237,7 @@ def test_weights4_bytes():
     assert size(E=2, Z=64, K=256, group=32) == 2 * 64 * 128 + 2 * 64 * 8 * 2
     assert size(E=2, Z=64, K=256, fmt=1, group=32) == 2 * 64 * 128 + 2 * 64 * 8
     assert size(E=2, Z=64, K=136) == size(E=2, Z=64, K=256)
-    assert size(E=1, Z=8, K=8) == 512 + 256
+    assert size(E=1, Z=8, K=8) == 1024 + 256     # 16 rows
 
 
 def test_expert_linear4_refusals():
