@@ -256,6 +256,7 @@ class Plan:
         self.workspace = None
         self.topk_idx = None
         self.device = None
+        self._configs = {}   # of norm, norm_backward and expert_linear4, by what they say
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -685,16 +686,24 @@ class Plan:
         if y is not None:
             _apart((y,), (x, w4.packed, bias, residual))
         y = _out(y, (rows, N), torch.bfloat16, "y", dev)
-        cfg = ctypes.byref(_abi.ExpertConfig(K, N, _abi.ACTIVATION[activation]))
+        cfg = self._configs.get((K, N, activation))
+        if cfg is None:
+            cfg = ctypes.byref(_abi.ExpertConfig(K, N, _abi.ACTIVATION[activation]))
+            self._configs[(K, N, activation)] = cfg
         self._launch("moe_expert_linear4", dev, cfg, w4.cfg, x.data_ptr(), w4.packed.data_ptr(),
                      _addr(bias), _addr(residual), y.data_ptr())
         return y
 
     # -- moe_norm
     def _norm_config(self, kind: str, eps: float, x: torch.Tensor, y_code: int):
-        if kind not in _abi.NORM:
-            raise ValueError(f"kind must be one of {tuple(_abi.NORM)}")
-        return ctypes.byref(_abi.NormConfig(_abi.NORM[kind], eps, _OUT_CODE[x.dtype], y_code))
+        """(config, bytes of norm_backward's workspace)"""
+        at = (kind, eps, x.dtype, y_code)
+        if at not in self._configs:     # making one takes 1 us, asking for the bytes another
+            if kind not in _abi.NORM:
+                raise ValueError(f"kind must be one of {tuple(_abi.NORM)}")
+            cfg = ctypes.byref(_abi.NormConfig(_abi.NORM[kind], eps, _OUT_CODE[x.dtype], y_code))
+            self._configs[at] = cfg, self._lib.moe_norm_backward_workspace_bytes(self._h, cfg)
+        return self._configs[at]
 
     @_on_stream
     def norm(self, x: torch.Tensor, gamma: torch.Tensor | None = None,
@@ -718,7 +727,7 @@ class Plan:
             _need(residual, (self.T, self.H), (x.dtype,), "residual", dev)
         elif total is not None:
             raise ValueError("total is written with a residual only")
-        cfg = self._norm_config(kind, eps, x, _out_code(out_dtype, "out_dtype"))
+        cfg, _ = self._norm_config(kind, eps, x, _out_code(out_dtype, "out_dtype"))
         if y is not None or total is not None or stats is not None:
             _apart((y, total, stats), (x, gamma, beta, residual))
         y = _out(y, (self.T, self.H), out_dtype, "y", dev)
@@ -755,9 +764,8 @@ class Plan:
             _need(gamma, (self.H,), _F32, "gamma", dev)
         if grad_total is not None:
             _need(grad_total, (self.T, self.H), (total.dtype,), "grad_total", dev)
-        cfg = self._norm_config(kind, 0.0, total, _OUT_CODE[grad_y.dtype])
+        cfg, need = self._norm_config(kind, 0.0, total, _OUT_CODE[grad_y.dtype])
         inputs = (grad_y, total, stats, gamma, grad_total)
-        need = self._lib.moe_norm_backward_workspace_bytes(self._h, cfg)
         if workspace is not None:
             _need(workspace, getattr(workspace, "shape", ()), (getattr(workspace, "dtype", None),),
                   "workspace", dev)

@@ -27,9 +27,11 @@ __device__ __forceinline__ float e2m1_scale(uint32_t byte) { return __uint_as_fl
 // under the exponent of 128.
 constexpr float kInt4Offset = 136.0f;  // 128 + c stands for c - 8
 __device__ __forceinline__ bf16x8 decode_int4(uint32_t codes) {
+  uint32_t magic = 0x43004300u;
+  asm("" : "+v"(magic));  // in a vector register: an instruction takes one constant of another kind
   u32x4 r;
 #pragma unroll
-  for (int p = 0; p < 4; ++p) r[p] = ((codes >> (4 * p)) & 0x000f000fu) | 0x43004300u;
+  for (int p = 0; p < 4; ++p) r[p] = ((codes >> (4 * p)) & 0x000f000fu) | magic;
   return __builtin_bit_cast(bf16x8, r);
 }
 
@@ -42,10 +44,12 @@ __device__ __forceinline__ bf16x8 decode_int4(uint32_t codes) {
 __device__ __forceinline__ bf16x8 decode_int4_scaled(uint32_t codes, float scale) {
   typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
   const float less = -1032.0f * scale;
+  uint32_t magic = 0x64006400u;
+  asm("" : "+v"(magic));  // in a vector register: an instruction takes one constant of another kind
   u32x4 r;
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
-    const f16x2 v = __builtin_bit_cast(f16x2, ((codes >> (4 * p)) & 0x000f000fu) | 0x64006400u);
+    const f16x2 v = __builtin_bit_cast(f16x2, ((codes >> (4 * p)) & 0x000f000fu) | magic);
     r[p] = bf16_pair(__builtin_fmaf((float)v[0], scale, less), __builtin_fmaf((float)v[1], scale, less));
   }
   return __builtin_bit_cast(bf16x8, r);
@@ -53,21 +57,40 @@ __device__ __forceinline__ bf16x8 decode_int4_scaled(uint32_t codes, float scale
 
 // ---- few rows an expert
 
-// Which expert a block of the few-rows kernels works on: `which`, or, where a batch (or band) has
-// fewer rows than experts, that of row `which` if it is the expert's first; else -1.
-__device__ __forceinline__ int few_rows_expert(const ExpertDims& x, const int32_t* off, int which) {
-  if (x.rows >= x.E) return which;
+// The expert that a block of the few-rows kernel works on: `which`, or, where a batch (or band) has
+// fewer rows than experts, that of row `which` if it is the expert's first (else no rows).  Its
+// offsets come out of the lanes that searched for it, not of further loads that wait for the first.
+struct Rows {
+  int e, first, count;
+};
+__device__ __forceinline__ Rows few_rows_of(const ExpertDims& x, const int32_t* off, int which) {
+  Rows r{which, 0, 0};
+  if (x.rows >= x.E) {
+    r.first = off[which];
+    r.count = off[which + 1] - r.first;
+    return r;
+  }
   const int lane = threadIdx.x % kWave;
-  const int row = off[0] + which;
   const int step = (x.E + kWave - 1) / kWave;
   const int e1 = lane * step;
-  int e = (__popcll(__ballot(e1 < x.E && off[min(e1, x.E)] <= row)) - 1) * step;
-  if (step > 1) {
-    const int e2 = e + lane;
-    e += __popcll(__ballot(lane < step && e2 < x.E && off[min(e2, x.E)] <= row)) - 1;
+  const int start = off[0], v1 = off[min(e1, x.E)], total = off[x.E];
+  const int row = start + which;
+  // Lane 0 is in; the last lane in has the expert, or the first of its `step` candidates.
+  const int at = __popcll(__ballot(e1 < x.E && v1 <= row)) - 1;
+  int next;
+  if (step == 1) {
+    r.e = at;
+    r.first = __builtin_amdgcn_readlane(v1, at);
+    next = at + 1 < kWave ? __builtin_amdgcn_readlane(v1, min(at + 1, kWave - 1)) : total;
+  } else {
+    const int e2 = at * step + lane, v2 = off[min(e2, x.E)];
+    const int in = __popcll(__ballot(lane < step && e2 < x.E && v2 <= row)) - 1;
+    r.e = at * step + in;
+    r.first = __builtin_amdgcn_readlane(v2, in);
+    next = __builtin_amdgcn_readlane(v2, in + 1);  // step <= 16
   }
-  e = __builtin_amdgcn_readfirstlane(e);
-  return off[e] == row ? e : -1;
+  if (r.first == row) r.count = next - row;
+  return r;
 }
 
 // A strip is 16 columns of y with a gated activation (16 weight rows of the gate and 16 of the up
@@ -129,9 +152,8 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void expert4_few_rows_kernel(
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const uint32_t block = base + blockIdx.x;  // below 2^26
-  const int e = few_rows_expert(x, off, (int)(block / (uint32_t)cut.shares));
-  if (e < 0) return;
-  const int o0 = off[e], rows = off[e + 1] - o0;
+  const Rows of = few_rows_of(x, off, (int)(block / (uint32_t)cut.shares));
+  const int e = of.e, o0 = of.first, rows = of.count;
   if (rows <= 0) return;
   const int strip = (int)(block % (uint32_t)cut.shares) * (F::kWaves / cut.split) + wave / cut.split;
   const int member = wave % cut.split;

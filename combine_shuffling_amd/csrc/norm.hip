@@ -262,7 +262,7 @@ __global__ __launch_bounds__(kMaxWaves * kWave) void norm_grad_kernel(
     const void* __restrict__ gtotal, void* __restrict__ gx, float* __restrict__ ggamma,
     float* __restrict__ gbeta) {
   __shared__ float slots[2][2][kMaxWaves];
-  extern __shared__ float sums[];  // [H] where a block has several rows at a time
+  extern __shared__ float sums[];  // [parts][H] where a block's sums come in several parts: 32 KiB at most
   const Place<L, CH> at(s);
   float w[CH][8], sg[CH][8], sb[CH][8];
 #pragma unroll
@@ -370,28 +370,17 @@ __global__ __launch_bounds__(kMaxWaves * kWave) void norm_grad_kernel(
     const int parts = L < kWave ? blockDim.x / kWave : s.rows;
     const int part = L < kWave ? at.first_wave : at.row;
     const bool mine = L == kWave || threadIdx.x % kWave < L;
-    if (parts == 1) {
+    float* own = parts == 1 ? to : sums + part * n.H;
 #pragma unroll
-      for (int i = 0; i < CH; ++i)
-        if (mine && at.live[i]) store(to, at.chunk[i], rounded<true>(v[i]));
-      return;
+    for (int i = 0; i < CH; ++i)
+      if (mine && at.live[i]) store(own, at.chunk[i], rounded<true>(v[i]));
+    if (parts == 1) return;
+    __syncthreads();
+    for (int c = threadIdx.x * 4; c < n.H; c += blockDim.x * 4) {
+      f32x4 t = *reinterpret_cast<const f32x4*>(sums + c);
+      for (int p = 1; p < parts; ++p) t += *reinterpret_cast<const f32x4*>(sums + p * n.H + c);
+      *reinterpret_cast<f32x4*>(to + c) = t;
     }
-    for (int p = 0; p < parts; ++p) {
-      if (p == part && mine) {
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          if (!at.live[i]) continue;
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            float& a = sums[at.chunk[i] * 8 + q];
-            a = p == 0 ? v[i][q] : a + v[i][q];
-          }
-        }
-      }
-      __syncthreads();
-    }
-    for (int c = threadIdx.x * 4; c < n.H; c += blockDim.x * 4)
-      *reinterpret_cast<f32x4*>(to + c) = *reinterpret_cast<const f32x4*>(sums + c);
     __syncthreads();
   };
   put(ggamma, sg);
@@ -493,11 +482,13 @@ hipError_t launch_norm_grad(const NormDims& n, const void* gy, const void* total
   float* pb = rows > 1 && gbeta ? partial + (int64_t)rows * n.H : gbeta;
   const int turns = (n.T + sp.rows - 1) / sp.rows;
   const int blocks = sums ? rows : std::min(turns, kCus);
-  const bool lds = sums && threads > sp.waves * kWave;
+  // A part for each of the block's rows (or waves of several rows) at a time.
+  const int parts = threads / (sp.waves * kWave);
+  const int lds = sums && parts > 1 ? parts * n.H * (int)sizeof(float) : 0;
   const hipError_t e = with_types(n, [&](auto xf, auto yf) {
     return with_widths(sp.chunks, [&](auto l, auto c) {
       return launch(MOE_KERNEL_NORM_GRAD, norm_grad_kernel<xf(), yf(), l(), c()>, dim3(blocks),
-                    dim3(threads), lds ? n.H * 4 : 0, s, n, sp, gy, total, stats, gamma, gtotal, gx,
+                    dim3(threads), lds, s, n, sp, gy, total, stats, gamma, gtotal, gx,
                     pg, pb);
     });
   });
