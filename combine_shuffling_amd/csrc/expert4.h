@@ -166,7 +166,7 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void expert4_few_rows_kernel(
 #pragma unroll
   for (int q = 0; q < 8; ++q) offset[q] = (__bf16)-kInt4Offset;
 
-  // A place in the wave's work: round, phase, and blocks [block, last) that are left of its part.
+  // A place in the wave's work: the phase, and blocks [block, last) that are left of its part of it.
   struct Cursor {
     int phase, block, last;
   };
@@ -420,7 +420,7 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void expert4_few_rows_kernel(
 // into bf16 while the products of the step before run.
 template <int G, bool E2M1, bool GATED_>
 struct Tile4 {
-  static constexpr int WM = 1, WN = 4, BM = WM * 128, BN = 256, MI = 8, NJ = 4;
+  static constexpr int WM = 1, WN = 4, BM = 128, BN = 256, MI = 8, NJ = 4;
   static constexpr bool GATED = GATED_;
   static constexpr int kNW = WM * WN, kThreads = kNW * kWave;
   static constexpr int kHalf = BM * 64;      // bytes of 32 along the contraction
@@ -448,15 +448,17 @@ struct Tile4 {
   uint32_t va[QA];     // byte offsets of this lane's loads of a stage
   uint32_t lda, codes_stride, scales_stride;
   char* lds;
-  int wave, lane, m0, K, blocks, second;
+  int wave, lane, K, blocks, second;
+  int at;              // byte offset of the lane's part of a half stage's first fragment
   int put;             // LDS offset of the stage that is read next
+  static constexpr int m0 = 0;  // every wave has all the rows of the tile
 
   __device__ __forceinline__ Tile4(char* lds_, const ExpertDims& x, const Weights4& w4)
       : lda((uint32_t)x.K * 2), codes_stride(w4.codes_stride()), scales_stride(w4.scales_stride()),
         lds(lds_), K(x.K), blocks(w4.blocks), second(x.N), put(0) {
     lane = threadIdx.x % kWave;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    m0 = wave / WN * 16;
+    at = (lane & 15) * 64 + (((lane >> 4) ^ swizzle(lane & 15)) << 4);
 #pragma unroll
     for (int q = 0; q < QA; ++q)
       va[q] = (uint32_t)((q % 2 * kNW + wave) * 16 + lane / 4) * lda + chunk() * 16 + q / 2 * 64;
@@ -539,11 +541,8 @@ struct Tile4 {
   template <int S>
   __device__ __forceinline__ void step(const char* from, int rows, const bf16x8 (&b)[NJ],
                                        bf16x8 (&then)[NJ], const Packed& p) {
-    const int i = lane & 15, g = lane >> 4;
-    auto read = [&](int m) {
-      const int r = m0 + m * (WM * 16) + i;
-      return *reinterpret_cast<const bf16x8*>(from + r * 64 + ((g ^ swizzle(r)) << 4));
-    };
+    const char* mine = from + at;
+    auto read = [&](int m) { return *reinterpret_cast<const bf16x8*>(mine + m * 1024); };
     bf16x8 a[2][2] = {{read(0), read(1)}, {}};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {

@@ -161,6 +161,35 @@ def test_products_of_integers_are_exact(T, E, k, K, N, kind, fmt, group, dev):
 
 
 @pytest.mark.parametrize("fmt,group", FORMATS, ids=IDS)
+@pytest.mark.parametrize("T,E,k,K,N,kind", [
+    (1, 6, 2, 7168, 40, "uniform"),      # few strips: eight waves share each
+    (16, 16, 2, 7168, 72, "uniform"),    # x of 4 rows at a time in LDS
+    (16, 2, 2, 7168, 24, "uniform"),     # of 16 rows, the contraction in phases
+    (30, 4, 3, 3000, 136, "uniform"),    # of 16 rows, two phases of unequal length
+    (3, 3, 1, 33000, 16, "uniform"),
+    (40, 2, 2, 5000, 136, "uniform"),    # passes of 32 rows, in phases
+    (90, 5, 4, 2048, 4104, "skewed"),
+    (300, 2, 2, 5000, 136, "uniform"),   # tiles
+    (700, 200, 8, 136, 24, "few"),       # tiles of all rows on few of the experts
+])
+def test_long_and_odd_products_of_integers_are_exact(T, E, k, K, N, kind, fmt, group, dev):
+    say(f"[experts4] exact, long T={T} E={E} k={k} K={K} N={N} {kind} {fmt} {group}")
+    rng = np.random.default_rng(T)
+    idx, off, x, codes, scales, b, _ = inputs(rng, T, E, k, K, N, kind, "swiglu", fmt, group, True)
+    plan = routed(idx, E, 1, 8, dev)
+    w, _ = block_ref.values4(codes, scales, fmt, group)
+    z = np.concatenate([x[off[e]: off[e + 1]] @ w[e].T + b[e] for e in range(E)])
+    assert np.abs(z).max() < 2 ** 20
+    # plain, the gate and the up projection side by side, then the up projection gated
+    w4, xd, bd = packed(codes, scales, fmt, group, dev), bf16(x, dev), torch.from_numpy(b.astype(np.float32)).to(dev)
+    assert np.array_equal(f64(plan.expert_linear4(xd, w4, bd)), rounded(z))
+    got = f64(plan.expert_linear4(xd, w4, bd, activation="swiglu"))
+    want = ref.act("swiglu", z[:, :N]) * z[:, N:]
+    # sigmoid's float32 roundings (as for bf16 weights) and one to bf16
+    assert (np.abs(got - want) <= (272 * ref.U + ref.BF16_HALF) * np.abs(want) + 1e-30).all()
+
+
+@pytest.mark.parametrize("fmt,group", FORMATS, ids=IDS)
 @pytest.mark.parametrize("T", [4, 37, 700])
 def test_values_that_are_not_finite_stay_in_their_rows(T, fmt, group, dev):
     rng = np.random.default_rng(T)
