@@ -39,9 +39,9 @@ hipError_t launch_norm_grad(const NormDims& n, const void* gy, const void* total
 // j is nibble j, as the conversion instruction takes them; INT4 weight 2p is nibble p and weight
 // 2p + 1 nibble p + 4, so that one shift and one mask leave a pair of them in the halves of a
 // register.
-// Scales (bf16 for INT4, a byte for E2M1) follow at a multiple of 256 bytes, tile by tile in the same
-// order: [16 rows][groups of the tile], so that a lane finds those of its row, or of the four
-// consecutive rows that its results are, side by side.
+// Scales follow at a multiple of 256 bytes, tile by tile in the same order, so that a lane finds those
+// of its row (E2M1, bytes: [16 rows][4 groups]), or of the four consecutive rows that its results are
+// (INT4, bf16: [16 rows], [16 rows][2 groups], or two of these with groups of 32), side by side.
 struct Weights4 {
   int32_t E, Z, K;
   int32_t e2m1;      // format
@@ -49,6 +49,8 @@ struct Weights4 {
   int32_t blocks;    // of 128 along K
   int32_t tiles;     // of 16 rows
   __host__ __device__ int given_groups() const { return (K + group - 1) / group; }
+  // Groups of a row whose scales are side by side.
+  __host__ __device__ int beside() const { return e2m1 ? 4 : group == 128 ? 1 : 2; }
   // Bytes of one tile of 16 rows along all of K.
   __host__ __device__ uint32_t codes_stride() const { return (uint32_t)blocks * 1024; }
   __host__ __device__ uint32_t scales_stride() const {

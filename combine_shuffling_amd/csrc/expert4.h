@@ -35,26 +35,6 @@ __device__ __forceinline__ bf16x8 decode_int4(uint32_t codes) {
   return __builtin_bit_cast(bf16x8, r);
 }
 
-// The same codes times a scale, in bf16: the matrix instructions of a tile of many rows take the
-// weights with their scales in them, since scaling sums of a group instead would take a second set of
-// accumulators, for which there are no registers.  scale * (c - 8) is rounded to bf16 (nearest
-// even), the one rounding of a weight; it is exact where the scale has five significant bits or fewer.
-// The codes are first put under the exponent of 1024 in float16, from where one mixed multiply-add
-// a code takes them: scale * (1024 + c) - 1032 * scale is exact in float32.
-__device__ __forceinline__ bf16x8 decode_int4_scaled(uint32_t codes, float scale) {
-  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-  const float less = -1032.0f * scale;
-  uint32_t magic = 0x64006400u;
-  asm("" : "+v"(magic));  // in a vector register: an instruction takes one constant of another kind
-  u32x4 r;
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const f16x2 v = __builtin_bit_cast(f16x2, ((codes >> (4 * p)) & 0x000f000fu) | magic);
-    r[p] = bf16_pair(__builtin_fmaf((float)v[0], scale, less), __builtin_fmaf((float)v[1], scale, less));
-  }
-  return __builtin_bit_cast(bf16x8, r);
-}
-
 // ---- few rows an expert
 
 // The expert that a block of the few-rows kernel works on: `which`, or, where a batch (or band) has
@@ -93,6 +73,29 @@ __device__ __forceinline__ Rows few_rows_of(const ExpertDims& x, const int32_t* 
   return r;
 }
 
+// INT4 scales of four consecutive weight rows, for a block of 128 along the contraction.
+template <int G>
+struct Int4Scales {
+  static constexpr int kGroups = 128 / G;
+  static constexpr int kRow = kGroups == 1 ? 2 : 4;  // bytes of a row's scales that are side by side
+  u32x4 v[(kGroups + 1) / 2];
+  // Those of groups q and q + 1 (of the only one); at: where the first row's for the block are.
+  __device__ __forceinline__ void load(const __amdgpu_buffer_rsrc_t& from, uint32_t at, int q) {
+    if constexpr (kGroups == 1) {
+      const u32x2 r = __builtin_amdgcn_raw_buffer_load_b64(from, at, 0, 0);
+      v[0][0] = r[0];
+      v[0][1] = r[1];
+    } else {
+      v[q / 2] = __builtin_amdgcn_raw_buffer_load_b128(from, at + q * 32, 0, 0);
+    }
+  }
+  // That of row r (0..3) for group q.
+  __device__ __forceinline__ float get(int r, int q) const {
+    const uint32_t w = kGroups == 1 ? v[0][r / 2] : v[q / 2][r];
+    return __uint_as_float((kGroups == 1 ? r : q) % 2 ? w & 0xffff0000u : w << 16);
+  }
+};
+
 // A strip is 16 columns of y with a gated activation (16 weight rows of the gate and 16 of the up
 // projection), else 32.  A block of eight waves works for one expert, on R of its rows at a time,
 // whose x it holds in LDS (the contraction in phases where it does not fit).  A wave, or `split` of
@@ -116,15 +119,8 @@ struct FewRows {
   // Codes and scales of U blocks of a strip.
   struct Step {
     u32x4 codes[U][2];
-    u32x2 si[E2M1 ? 1 : U][2][kGroups];  // INT4: the scales of the lane's four result columns, a
-                                         // column's groups side by side
-    uint32_t se[E2M1 ? U : 1][2];        // E2M1: those of the lane's weight row
-    // Scale of result column c for group q of block u.
-    __device__ __forceinline__ float scale(int u, int h, int c, int q) const {
-      const int at = c * kGroups + q;
-      const uint32_t v = si[u][h][at / 4][at / 2 % 2];
-      return __uint_as_float(at % 2 ? v & 0xffff0000u : v << 16);
-    }
+    Int4Scales<G> si[E2M1 ? 1 : U][2];  // INT4: those of the lane's four result columns
+    uint32_t se[E2M1 ? U : 1][2];       // E2M1: those of the lane's weight row
   };
 };
 
@@ -186,23 +182,16 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void expert4_few_rows_kernel(
       const uint32_t r = row + i, q4 = row + g * 4;
       const uint32_t vw = (r >> 4) * w4.codes_stride() + ((r & 15) | g << 4) * 16;
       const uint32_t vs = E2M1 ? (r >> 4) * w4.scales_stride() + (r & 15) * 4
-                               : (q4 >> 4) * w4.scales_stride() + (q4 & 15) * kGroups * 2;
+                               : (q4 >> 4) * w4.scales_stride() + (q4 & 15) * Int4Scales<G>::kRow;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const uint32_t b = (uint32_t)min(c.block + u, c.last - 1);  // (past the end: not multiplied)
         t.codes[u][h] = __builtin_amdgcn_raw_buffer_load_b128(rw, vw + b * 1024, 0, 0);
         if constexpr (E2M1) {
           t.se[u][h] = __builtin_amdgcn_raw_buffer_load_b32(rs, vs + b * 64, 0, 0);
-        } else if constexpr (kGroups == 1) {
-          t.si[u][h][0] = __builtin_amdgcn_raw_buffer_load_b64(rs, vs + b * 32, 0, 0);
         } else {
 #pragma unroll
-          for (int q = 0; q < kGroups; q += 2) {
-            const u32x4 v =
-                __builtin_amdgcn_raw_buffer_load_b128(rs, vs + b * (kGroups * 32) + q * 8, 0, 0);
-            t.si[u][h][q] = u32x2{v[0], v[1]};
-            t.si[u][h][q + 1] = u32x2{v[2], v[3]};
-          }
+          for (int q = 0; q < kGroups; q += 2) t.si[u][h].load(rs, vs + b * (kGroups * 32), q);
         }
       }
     }
@@ -297,7 +286,7 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void expert4_few_rows_kernel(
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
               for (int c4 = 0; c4 < 4; ++c4) {
-                const float scale = t.scale(u, h, c4, q);
+                const float scale = t.si[u][h].get(c4, q);
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
                   acc[m][h][c4] = __builtin_fmaf(scale, sum[m][h][c4], acc[m][h][c4]);
@@ -412,112 +401,128 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void expert4_few_rows_kernel(
 
 // ---- many rows an expert
 
-// A block computes tiles of BM rows x 256 columns, one after another, as the products of bf16
+// A block computes tiles of 64 or 128 rows x 256 columns, one after another, as the products of bf16
 // weights do (the order of the tiles, of a wave's rows and columns, and the epilogue are the same).
-// x goes straight to LDS, in stages of 64 along the contraction, three deep.  The weights do not
-// pass through LDS: a wave loads the codes of its own 64 columns into registers, a block of 128 along
-// the contraction ahead (a fourth of what bf16 takes), and turns eight codes a lane and fragment
-// into bf16 while the products of the step before run.
-template <int G, bool E2M1, bool GATED_>
+// x goes straight to LDS, in stages of 128 along the contraction.  The weights do not pass through
+// LDS: a wave loads the codes of its own 64 columns into registers, a block of 128 along the
+// contraction ahead (a fourth of what bf16 takes), and turns eight codes a lane and fragment into
+// bf16 while another block's products run.
+//
+// INT4: no weight is rounded.  A group's products with 128 + c are added up in sums of their own,
+// which start from its products with -136 and so come to those with c - 8, and the scale multiplies
+// the finished sums into the accumulators.  A wave takes 16 rows x 64 columns at a time through a
+// group, whose fragments it has expanded, so that the sums take 16 registers; tiles of 64 rows leave
+// room for them.  With 128 rows registers run out (425 us for 64 experts, top-8, 4096 tokens, 2048 ->
+// 2 x 1024, against 332), and with groups of 32, whose scales take a quarter of the registers, they
+// do with 64 rows too (3200 us; the kernel for few rows takes 740).
+//
+// E2M1 weights are bf16 numbers, scale and all.  Tiles of 128 rows where there are four a CU: 252 us
+// for that example, 439 for 8 experts, top-2, 8192 tokens, 4096 -> 4096, against 314 and 514 with 64
+// rows, which leave fewer products for each weight that is expanded; where there are fewer tiles, 64
+// rows: 68 us against 82 for 512 tokens of the latter, 27 against 33 for 1021 tokens, top-4 of 30, 776
+// -> 1000.
+//
+// What bounds the large products: the matrix cores are busy half of the time; expanding codes and
+// scaling sums take as many cycles of the vector units, which two waves a SIMD overlap in part.
+template <int G, bool E2M1, bool GATED_, int MI_>
 struct Tile4 {
-  static constexpr int WM = 1, WN = 4, BM = 128, BN = 256, MI = 8, NJ = 4;
+  static constexpr int WM = 1, WN = 4, MI = MI_, BM = MI * 16, BN = 256, NJ = 4;
   static constexpr bool GATED = GATED_;
   static constexpr int kNW = WM * WN, kThreads = kNW * kWave;
-  static constexpr int kHalf = BM * 64;      // bytes of 32 along the contraction
-  static constexpr int kStage = 2 * kHalf, kStages = 3, kLds = kStages * kStage;
-  static constexpr int QA = kStage / 1024 / kNW;  // loads a wave and stage
-  static constexpr int kQuarter = BM / 4;
-  static constexpr int kGroups = 128 / G;         // scales of a row and block
-  static constexpr int kScaleBytes = kGroups * (E2M1 ? 1 : 2);
-  static constexpr int kPacked = 2 * NJ;         // loads of codes and scales a wave and block
+  static constexpr int kStage = BM * 256, kStages = MI == 8 ? 2 : 3, kLds = kStages * kStage;
+  static constexpr int kAhead = kStages - 1;      // blocks of x that are under way
+  static constexpr int QA = kStage / 1024 / kNW;  // loads of x a wave and block
+  static constexpr int kGroups = 128 / G;         // groups of a row and block
+  static constexpr int kSteps = G / 32;           // matrix instructions a group and fragment
+  static constexpr int kBlocksACu = E2M1 && GATED && MI == 4 ? 3 : 2;
+  static constexpr int m0 = 0;  // every wave has all the rows of the tile
 
-  // Codes and scales of a block of 128 of the wave's columns.
+  // Codes of a block of 128 of the wave's columns, and the scales of the lane's results.
   struct Packed {
     u32x4 codes[NJ];
-    uint32_t scales[NJ][(kScaleBytes + 3) / 4];
+    std::conditional_t<E2M1, uint32_t, Int4Scales<G>> scales[NJ];
   };
-  // What is loaded next: a block of 128 of a tile.
-  struct Cursor {
-    const char *a, *codes, *scales;            // the tile's first row; the expert's weights
-    uint32_t a_bytes, codes_bytes, scales_bytes;
-    int n0;                                    // the tile's first column of y
+  // A place in the block's work: a tile, and a block of 128 of it.
+  struct Walk {
+    int number;   // of the tile after
+    Segment s;    // the tile's rows (none: no tile is left)
+    int n0;       // its first column of y
     int block;
   };
 
   f32x4 acc[MI][NJ];
-  uint32_t va[QA];     // byte offsets of this lane's loads of a stage
-  uint32_t lda, codes_stride, scales_stride;
-  char* lds;
+  const char *x, *codes, *scales;
+  uint32_t lda, codes_stride, scales_stride, codes_bytes, scales_bytes;
   int wave, lane, K, blocks, second;
-  int at;              // byte offset of the lane's part of a half stage's first fragment
-  int put;             // LDS offset of the stage that is read next
-  static constexpr int m0 = 0;  // every wave has all the rows of the tile
+  uint32_t va;       // byte offset of this lane's first load of a block of x
+  uint32_t from_[4]; // byte offsets of the lane's fragments s of the first 16 rows of a stage
+  int put;           // LDS offset of the stage that is read next
+  bf16x8 offset;
 
-  __device__ __forceinline__ Tile4(char* lds_, const ExpertDims& x, const Weights4& w4)
-      : lda((uint32_t)x.K * 2), codes_stride(w4.codes_stride()), scales_stride(w4.scales_stride()),
-        lds(lds_), K(x.K), blocks(w4.blocks), second(x.N), put(0) {
+  __device__ __forceinline__ Tile4(const ExpertDims& d, const Weights4& w4, const char* x_,
+                                      const char* codes_, const char* scales_)
+      : x(x_), codes(codes_), scales(scales_), lda((uint32_t)d.K * 2), codes_stride(w4.codes_stride()),
+        scales_stride(w4.scales_stride()), codes_bytes(w4.tiles * w4.codes_stride()),
+        scales_bytes(w4.tiles * w4.scales_stride()), K(d.K), blocks(w4.blocks), second(d.N), put(0) {
     lane = threadIdx.x % kWave;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    at = (lane & 15) * 64 + (((lane >> 4) ^ swizzle(lane & 15)) << 4);
+    const int i = lane & 15, g = lane >> 4;
+    va = (uint32_t)(wave * 4 + g) * lda + chunk() * 16;
 #pragma unroll
-    for (int q = 0; q < QA; ++q)
-      va[q] = (uint32_t)((q % 2 * kNW + wave) * 16 + lane / 4) * lda + chunk() * 16 + q / 2 * 64;
-    static_assert(QA == 4 && BM / 16 == 2 * kNW);
+    for (int s = 0; s < 4; ++s) from_[s] = i * 256 + (((s * 4 + g) ^ i) << 4);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) offset[q] = (__bf16)-kInt4Offset;
   }
 
-  // LDS row r of a half stage (64 bytes) holds chunk p ^ swizzle(r) at position p.
-  static __device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 3; }
-  __device__ __forceinline__ int chunk() const { return (lane & 3) ^ swizzle(lane / 4); }
+  // A stage has rows of 256 bytes, 16 chunks; position p of row r holds chunk p ^ r (of the lower
+  // four bits).  A load of a wave takes four rows, row 16 q + 4 wave + lane / 16 for its q-th.
+  __device__ __forceinline__ int chunk() const { return (lane & 15) ^ (wave * 4 + (lane >> 4)); }
 
-  // Codes and scales of the cursor's block.  Fragment j of a wave has the columns 32 (j / 2) + 8 g +
-  // 4 (j % 2) + 0..3 of its 64 in lane group g of the results (of the gate for j < 2 and of the up
-  // projection else, where gated), so lane i of the operand has the weight row of the column with
-  // g = i / 4 and i % 4.
-  __device__ __forceinline__ void load_packed(Packed& p, const Cursor& c) const {
-    const __amdgpu_buffer_rsrc_t rw = uniform_buffer(c.codes, c.codes_bytes);
-    const __amdgpu_buffer_rsrc_t rs = uniform_buffer(c.scales, c.scales_bytes);
+  __device__ __forceinline__ void load_x(const Walk& w, char* to) const {
+    const uint32_t done = (uint32_t)w.block * 256, bytes = (uint32_t)w.s.rows * lda;
+    const __amdgpu_buffer_rsrc_t r =
+        uniform_buffer(x + (int64_t)w.s.row * lda + done, bytes > done ? bytes - done : 0);
+    // Chunks past the end of the contraction read as zeros.
+    const bool in = w.block * 128 + chunk() * 8 < K;
+#pragma unroll
+    for (int q = 0; q < QA; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void*)(to + (q * kNW + wave) * 1024), 16,
+                                               in ? va + q * 16 * lda : kPast, 0, 0, 0);
+  }
+
+  // Fragment j of a wave has the columns 32 (j / 2) + 8 g + 4 (j % 2) + 0..3 of its 64 in lane group g
+  // of the results (of the gate for j < 2 and of the up projection else, where gated), so lane i of
+  // the operand has the weight row of the column with g = i / 4 and i % 4.
+  __device__ __forceinline__ int first_column(const Walk& w, int j) const {
+    return w.n0 + wave * (GATED ? 32 : 64) + j % 2 * 4 + j / 2 * (GATED ? second : 32);
+  }
+  __device__ __forceinline__ void load_codes(u32x4 (&c)[NJ], const Walk& w) const {
+    const __amdgpu_buffer_rsrc_t rw =
+        uniform_buffer(codes + (int64_t)w.s.e * codes_bytes, w.s.rows > 0 ? codes_bytes : 0);
     const int i = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int col = c.n0 + wave % WN * (GATED ? 32 : 64) + i / 4 * 8 + j % 2 * 4 + i % 4;
-      const uint32_t r = (uint32_t)(col + j / 2 * (GATED ? second : 32));
-      p.codes[j] = __builtin_amdgcn_raw_buffer_load_b128(
-          rw, (r >> 4) * codes_stride + c.block * 1024 + ((r & 15) | g << 4) * 16, 0, 0);
-      const uint32_t vs = (r >> 4) * scales_stride + (c.block * 16 + (r & 15)) * kScaleBytes;
-      if constexpr (kScaleBytes == 2) {
-        p.scales[j][0] = __builtin_amdgcn_raw_buffer_load_b16(rs, vs, 0, 0);
-      } else if constexpr (kScaleBytes == 4) {
-        p.scales[j][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, vs, 0, 0);
-      } else {
-        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(rs, vs, 0, 0);
-        p.scales[j][0] = v[0];
-        p.scales[j][1] = v[1];
-      }
+      const uint32_t r = (uint32_t)(first_column(w, j) + i / 4 * 8 + i % 4);
+      c[j] = __builtin_amdgcn_raw_buffer_load_b128(
+          rw, (r >> 4) * codes_stride + w.block * 1024 + ((r & 15) | g << 4) * 16, 0, 0);
     }
   }
-
-  // Loads half `h` of the cursor's block of x into the stage at `to`.
-  __device__ __forceinline__ void load_x(const Cursor& c, int h, char* to) const {
-    const int done = c.block * 128 + h * 64;
-    const __amdgpu_buffer_rsrc_t r = uniform_buffer(
-        c.a + (int64_t)done * 2, c.a_bytes > (uint32_t)done * 2 ? c.a_bytes - (uint32_t)done * 2 : 0);
+  // (E2M1: of the lane's weight rows; INT4: of its results.)
+  __device__ __forceinline__ void load_scales(decltype(Packed::scales)& v, const Walk& w) const {
+    const __amdgpu_buffer_rsrc_t rs =
+        uniform_buffer(scales + (int64_t)w.s.e * scales_bytes, w.s.rows > 0 ? scales_bytes : 0);
+    const int i = lane & 15, g = lane >> 4;
 #pragma unroll
-    for (int q = 0; q < QA; ++q) {
-      // Chunks past the end of the contraction read as zeros.
-      const bool in = done + q / 2 * 32 + chunk() * 8 < K;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void*)(to + (q * kNW + wave) * 1024), 16,
-                                               in ? va[q] : kPast, 0, 0, 0);
-    }
-  }
-
-  // Fragment j of step s (32 along the contraction) of a block.
-  static __device__ __forceinline__ bf16x8 decode(const Packed& p, int j, int s) {
-    if constexpr (E2M1) {
-      return decode_e2m1(p.codes[j][s], e2m1_scale((p.scales[j][0] >> (8 * s)) & 0xffu));
-    } else {
-      const int q = s * 32 / G;
-      const uint32_t v = p.scales[j][q / 2];
-      return decode_int4_scaled(p.codes[j][s], __uint_as_float(q % 2 ? v & 0xffff0000u : v << 16));
+    for (int j = 0; j < NJ; ++j) {
+      if constexpr (E2M1) {
+        const uint32_t r = (uint32_t)(first_column(w, j) + i / 4 * 8 + i % 4);
+        v[j] = __builtin_amdgcn_raw_buffer_load_b32(
+            rs, (r >> 4) * scales_stride + (w.block * 16 + (r & 15)) * 4, 0, 0);
+      } else {
+        const uint32_t c = (uint32_t)(first_column(w, j) + g * 8);
+        v[j].load(rs,
+                  (c >> 4) * scales_stride + w.block * (kGroups * 32) + (c & 15) * Int4Scales<G>::kRow, 0);
+      }
     }
   }
 
@@ -536,81 +541,137 @@ struct Tile4 {
     __builtin_amdgcn_sched_barrier(0);
   }
 
-  // One step of 32: products of the fragments b with x at `from`, and the fragments of step S of p.
-  // rows: rows of the tile that there are (the products of absent quarters are skipped).
-  template <int S>
-  __device__ __forceinline__ void step(const char* from, int rows, const bf16x8 (&b)[NJ],
-                                       bf16x8 (&then)[NJ], const Packed& p) {
-    const char* mine = from + at;
-    auto read = [&](int m) { return *reinterpret_cast<const bf16x8*>(mine + m * 1024); };
-    bf16x8 a[2][2] = {{read(0), read(1)}, {}};
+  // Products of a block with x at `from`, under the loads of x kAhead blocks on (wx), to another
+  // stage, which saying so (restrict) keeps the reads from waiting for, and those of the next block's
+  // codes and scales (wp), which take the place of this block's: the scales when all are used, which
+  // saves registers.  rows: rows of the tile that there are (products of 16 rows that are all absent
+  // are skipped).
+  __device__ __forceinline__ void multiply(const Walk& wx, const Walk& wp, char* __restrict__ to,
+                                           const char* __restrict__ from, int rows, Packed& p) {
+    u32x4 then[NJ];
+    load_codes(then, wp);
+    load_x(wx, to);
+    auto fragment = [&](int i, int s) {
+      return *reinterpret_cast<const bf16x8*>(from + i * 4096 + from_[s]);
+    };
+    if constexpr (E2M1) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (q < 3) {
-        a[(q + 1) % 2][0] = read(2 * q + 2);
-        a[(q + 1) % 2][1] = read(2 * q + 3);
-      }
-      if (q == 0 || rows > q * kQuarter) {
+      for (int s = 0; s < 4; ++s) {
+        bf16x8 b[NJ];
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int j = 0; j < NJ; ++j)
+          b[j] = decode_e2m1(p.codes[j][s], e2m1_scale((p.scales[j] >> (8 * s)) & 0xffu));
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          if (i > 0 && rows <= i * 16) break;
+          const bf16x8 a = fragment(i, s);
 #pragma unroll
           for (int j = 0; j < NJ; ++j)
-            acc[2 * q + m][j] =
-                __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], a[q % 2][m], acc[2 * q + m][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], a, acc[i][j], 0, 0, 0);
+        }
       }
-      then[q] = decode(p, q, S);
-      __builtin_amdgcn_sched_barrier(0);
+    } else {
+#pragma unroll
+      for (int q = 0; q < kGroups; ++q) {
+        bf16x8 b[kSteps][NJ];
+        float scale[NJ][4];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s) b[s][j] = decode_int4(p.codes[j][q * kSteps + s]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) scale[j][r] = p.scales[j].get(r, q);
+        }
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          if (i > 0 && rows <= i * 16) break;
+          f32x4 less = {0.0f, 0.0f, 0.0f, 0.0f}, part[NJ];
+          bf16x8 a[kSteps];
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s) {
+            a[s] = fragment(i, q * kSteps + s);
+            less = __builtin_amdgcn_mfma_f32_16x16x32_bf16(offset, a[s], less, 0, 0, 0);
+          }
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+              part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[s][j], a[s], s == 0 ? less : part[j],
+                                                                0, 0, 0);
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[i][j][r] = __builtin_fmaf(scale[j][r], part[j][r], acc[i][j][r]);
+        }
+      }
     }
+    __builtin_amdgcn_sched_barrier(0);
+    load_scales(p.scales, wp);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) p.codes[j] = then[j];
   }
 
-  // Half of a block: its two steps, under the loads of the same half of the cursor's block.  The two
-  // stages are different ones, and saying so (restrict) keeps the reads from waiting for the loads.
-  template <int H>
-  __device__ __forceinline__ void half(const Cursor& c, char* __restrict__ to,
-                                       const char* __restrict__ from, int rows, bf16x8 (&b)[NJ],
-                                       const Packed& now, const Packed& then) {
-    load_x(c, H, to);
-    bf16x8 f[NJ];
-    step<2 * H + 1>(from, rows, b, f, now);
-    step<H == 0 ? 2 : 0>(from + kHalf, rows, f, b, H == 0 ? now : then);
-  }
-
-  // acc = x w^T of a tile.  now: its first block's codes, b: the fragments of its first step; both
-  // are the next tile's afterwards.  next(cursor) sets the cursor to the block after.
-  // Order of a wave's loads: a block's codes and scales, its first half of x, its second half; a
-  // half is waited for one half before the next is asked for.
-  template <typename Next>
-  __device__ __forceinline__ void run(Cursor& c, const Next& next, int rows, Packed& now,
-                                      bf16x8 (&b)[NJ]) {
+  // acc = x w^T of a tile of `rows` rows.  now: codes and scales of its first block, and of the next
+  // tile's afterwards.  advance(walk) goes to the block after: wp is that of the codes that are
+  // loaded next, a block ahead, and wx that of x, kAhead ahead.
+  template <typename Advance>
+  __device__ __forceinline__ void run(char* lds, Walk& wx, Walk& wp, const Advance& advance, int rows,
+                                      Packed& now) {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     for (int n = 0; n < blocks; ++n) {
-      // The tile's first block had landed before the last epilogue.
-      if (n == 0)
+      // A tile's first kAhead blocks of x had landed before the last epilogue.  After a later one's
+      // loads came scales, and those of a whole block where two are under way.
+      if (n < kAhead)
         wait_and_meet<-1>();
       else
-        wait_and_meet<QA>();
-      Packed then;
-      load_packed(then, c);
-      const int second_half = stage_after(put), free = stage_after(second_half);
-      half<0>(c, lds + free, lds + put, rows, b, now, then);
-      if (n == 0)
-        wait_and_meet<-1>();
-      else
-        wait_and_meet<QA + kPacked>();
-      half<1>(c, lds + put, lds + second_half, rows, b, now, then);
-      put = free;
-      now = then;
-      next(c);
+        wait_and_meet<kAhead == 1 ? NJ : NJ + QA + 2 * NJ>();
+      const int next = stage_after(put);
+      multiply(wx, wp, lds + (kAhead == 1 ? next : stage_after(next)), lds + put, rows, now);
+      put = next;
+      advance(wx);
+      advance(wp);
     }
+    // The next tile's first blocks have landed before the epilogue's stores are issued.
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
 };
 
+// The epilogue of a tile: bias, activation, residual, and y.
 template <typename P>
-__global__ __launch_bounds__(P::kThreads, 2) void expert4_rows_kernel(
+__device__ __forceinline__ void tile4_epilogue(const P& p, const ExpertDims& x, const Segment& s,
+                                               int col0, const float* bias, const uint16_t* residual,
+                                               uint16_t* y) {
+  const int g = p.lane >> 4;
+  const int c0 = col0 + p.wave % P::WN * (P::GATED ? 32 : 64) + g * 8;
+  float bz[16];
+#pragma unroll
+  for (int q = 0; q < 16; ++q) bz[q] = 0.0f;
+  if (bias != nullptr) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int col = P::GATED ? c0 : c0 + h * 32;
+      if (col < x.N) {
+        const f32x4* q =
+            reinterpret_cast<const f32x4*>(bias + (int64_t)s.e * x.Z + col + (P::GATED ? h * x.N : 0));
+        const f32x4 lo = q[0], hi = q[1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          bz[h * 8 + i] = lo[i];
+          bz[h * 8 + 4 + i] = hi[i];
+        }
+      }
+    }
+  }
+  rows_epilogue<P, 0>(p, x, s, c0, bz, residual, y, nullptr);
+  if constexpr (P::MI > 4) rows_epilogue<P, 4>(p, x, s, c0, bz, residual, y, nullptr);
+}
+
+template <typename P>
+__global__ __launch_bounds__(P::kThreads, P::kBlocksACu) void expert4_rows_kernel(
     ExpertDims x, Weights4 w4, const int32_t* __restrict__ off, const char* __restrict__ a,
     const char* __restrict__ codes, const char* __restrict__ scales, const float* __restrict__ bias,
     const uint16_t* __restrict__ residual, uint16_t* __restrict__ y, int ntiles) {
@@ -620,95 +681,53 @@ __global__ __launch_bounds__(P::kThreads, 2) void expert4_rows_kernel(
   table.build<P::BM, P::kThreads>(off, x.E);
   const TileGrid<P::BM, P::BN> grid(1, __builtin_amdgcn_readfirstlane(table.first[x.E]), ntiles);
   const int numbers = grid.numbers();
-  const uint32_t ld = (uint32_t)x.K * 2;
-  int number = blockIdx.x;
-  Segment ahead{0, 0, 0};
-  const uint32_t codes_bytes = w4.tiles * w4.codes_stride(), scales_bytes = w4.tiles * w4.scales_stride();
-  typename P::Cursor c{a, codes, scales, 0, 0, 0, 0, -1};
-  // The block after the cursor's: at a tile's end the first of the next tile, if there is one (else
-  // of none: it loads nothing).
-  auto next = [&](typename P::Cursor& c) {
-    if (c.block >= 0 && ++c.block < w4.blocks) return;
-    c = {a, codes, scales, 0, 0, 0, 0, 0};
-    ahead.rows = 0;
-    for (; number < numbers; number += gridDim.x) {
-      const Tile t = grid.at(number);
+  typename P::Walk w{(int)blockIdx.x, {0, 0, 0}, 0, 0};
+  auto enter = [&](typename P::Walk& w) {  // the next tile
+    w.s.rows = w.block = 0;
+    for (; w.number < numbers; w.number += gridDim.x) {
+      const Tile t = grid.at(w.number);
       if (!t.live) continue;
-      const Segment s = ahead = segment_of<P::BM>(table, off, x.E, t.m);
-      c.a = a + (int64_t)s.row * ld;
-      c.a_bytes = (uint32_t)s.rows * ld;
-      c.codes = codes + (int64_t)s.e * codes_bytes;
-      c.scales = scales + (int64_t)s.e * scales_bytes;
-      c.codes_bytes = codes_bytes;
-      c.scales_bytes = scales_bytes;
-      c.n0 = t.n * kCols;
-      number += gridDim.x;
+      w.s = segment_of<P::BM>(table, off, x.E, t.m);
+      w.n0 = t.n * kCols;
+      w.number += gridDim.x;
       break;
     }
   };
-  next(c);
-  if (ahead.rows <= 0) return;
-  P p(lds, x, w4);
+  auto advance = [&](typename P::Walk& w) {
+    if (++w.block >= w4.blocks) enter(w);
+  };
+  enter(w);
+  if (w.s.rows <= 0) return;
+  P p(x, w4, a, codes, scales);
+  typename P::Walk wx = w, wp = w;
   typename P::Packed packed;
-  bf16x8 b[P::NJ];
-  p.load_packed(packed, c);
-  p.load_x(c, 0, lds);
-  p.load_x(c, 1, lds + P::kStage);
-#pragma unroll
-  for (int j = 0; j < P::NJ; ++j) b[j] = P::decode(packed, j, 0);
-  Segment s = ahead;
-  int col0 = c.n0;
-  next(c);
+  p.load_codes(packed.codes, wp);
+  p.load_scales(packed.scales, wp);
+  advance(wp);
+  for (int n = 0; n < P::kAhead; ++n) {
+    p.load_x(wx, lds + n * P::kStage);
+    advance(wx);
+  }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  while (s.rows > 0) {
-    Segment loaded = ahead;  // tile of the block that was loaded last: after run the next tile
-    int loaded_col0 = c.n0;
-    auto step = [&](typename P::Cursor& q) {
-      loaded = ahead;
-      loaded_col0 = q.n0;
-      next(q);
-    };
-    p.run(c, step, s.rows, packed, b);
-
-    const int g = p.lane >> 4;
-    const int c0 = col0 + p.wave % P::WN * (P::GATED ? 32 : 64) + g * 8;
-    float bz[16];
-#pragma unroll
-    for (int q = 0; q < 16; ++q) bz[q] = 0.0f;
-    if (bias != nullptr) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int col = P::GATED ? c0 : c0 + h * 32;
-        if (col < x.N) {
-          const f32x4* q = reinterpret_cast<const f32x4*>(bias + (int64_t)s.e * x.Z + col +
-                                                          (P::GATED ? h * x.N : 0));
-          const f32x4 lo = q[0], hi = q[1];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            bz[h * 8 + i] = lo[i];
-            bz[h * 8 + 4 + i] = hi[i];
-          }
-        }
-      }
-    }
-    rows_epilogue<P, 0>(p, x, s, c0, bz, residual, y, nullptr);
-    rows_epilogue<P, 4>(p, x, s, c0, bz, residual, y, nullptr);
-    s = loaded;
-    col0 = loaded_col0;
+  while (w.s.rows > 0) {
+    p.run(lds, wx, wp, advance, w.s.rows, packed);
+    tile4_epilogue(p, x, w.s, w.n0, bias, residual, y);
+    enter(w);
   }
 }
 
-// The kernel for few rows is taken up to 20 rows an expert on average, and up to 96 where the tiles
-// would leave half of the CUs without one.  Its passes take 16 rows where no expert has more or
-// they have up to 12 on average, else 32.  In us, passes of 16, of 32, and tiles, INT4 in groups of
-// 128 (E2M1): 64 experts, top-8, 2048 -> 2 x 1024: 16 tokens 26, 35, 48 (24, 28, 35), 64 tokens 34,
-// 39, 48, 128 tokens 47, 41, 48 (42, 35, 38), 256 tokens 72, 69, 55 (66, 56, 44); 30 experts, top-2,
-// 4096 -> 4096: 128 tokens 64, 74, 91, 256 tokens 95, 77, 90, 512 tokens 143, 135, 102; 8 experts of
-// those: 256 tokens 85, 66, 84, 512 tokens 146, 108, 92.
-bool few4(const ExpertDims& x) {
+// The kernel for few rows is taken up to 6 rows an expert on average, up to 80 where the tiles would
+// leave half of the CUs without one, and always with INT4 in groups of 32 (Tile4).  Its passes take
+// 16 rows where no expert has more or they have up to 12 on average, else 32.  In us, passes of 16, of
+// 32, and tiles of 64 rows, INT4 in groups of 128 (E2M1): 64 experts, top-8, 2048 -> 2 x 1024: 8 tokens
+// 22, 30, 28 (20, 24, 27), 48 tokens 28, 36, 31 (27, 33, 30), 64 tokens 33, 38, 30 (31, 32, 29), 256
+// tokens 69, 67, 40 (67, 55, 37); 30 experts, top-2, 4096 -> 4096: 32 tokens 48, 63, 52 (46, 55, 50), 64
+// tokens 56, 70, 55 (55, 61, 53); 8 experts of those, with 128 tiles: 64 tokens 34, 25, 41 (31, 23, 38),
+// 256 tokens 82, 64, 74 (73, 55, 63), 512 tokens 139, 106, 75 (122, 90, 65).
+bool few4(const ExpertDims& x, const Weights4& w4) {
   const int tiles = ceil_div(x.N, gated(x.act) ? 128 : 256);
-  return x.T <= 32 || (int64_t)x.rows <= (int64_t)x.E * 20 ||
-         ((int64_t)x.rows <= (int64_t)x.E * 96 && (int64_t)x.E * tiles <= kCus / 2);
+  return (!w4.e2m1 && w4.group == 32) || (int64_t)x.rows <= (int64_t)x.E * 6 ||
+         ((int64_t)x.rows <= (int64_t)x.E * 80 && (int64_t)x.E * tiles <= kCus / 2);
 }
 
 hipError_t expert_rows4(const ExpertDims& x, const Weights4& w4, const int32_t* off,
@@ -759,11 +778,20 @@ hipError_t expert_rows4(const ExpertDims& x, const Weights4& w4, const int32_t* 
                     dim3(P::kThreads), 0, s, x, w4, off, reinterpret_cast<const char*>(a), codes, scales,
                     bias, residual, y, ntiles);
     };
-    if (few4(x)) {
+    if (few4(x, w4)) {
       if (x.T <= 16 || (int64_t)x.rows <= (int64_t)x.E * 12) return few(std::integral_constant<int, 1>());
       return few(std::integral_constant<int, 2>());
     }
-    return gated(x.act) ? tiles(Type<Tile4<G, E2M1, true>>()) : tiles(Type<Tile4<G, E2M1, false>>());
+    if constexpr (E2M1) {
+      if ((int64_t)x.rows * ceil_div(x.N, gated(x.act) ? 128 : 256) >= 128 * 4 * kCus)
+        return gated(x.act) ? tiles(Type<Tile4<G, E2M1, true, 8>>())
+                            : tiles(Type<Tile4<G, E2M1, false, 8>>());
+    }
+    if constexpr (E2M1 || G > 32)
+      return gated(x.act) ? tiles(Type<Tile4<G, E2M1, true, 4>>())
+                          : tiles(Type<Tile4<G, E2M1, false, 4>>());
+    else
+      return hipErrorInvalidValue;  // (few4 takes them all)
   };
   if (w4.e2m1) return by_rows(std::integral_constant<int, 32>(), std::true_type());
   if (w4.group == 32) return by_rows(std::integral_constant<int, 32>(), std::false_type());

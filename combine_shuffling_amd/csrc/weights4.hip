@@ -47,7 +47,8 @@ struct At {
   __device__ __forceinline__ int k(int s) const { return k0 + 32 * s + 8 * g; }
   // Index of the scale of weights k(s).
   __device__ __forceinline__ int64_t scale(const Weights4& w, int s) const {
-    return (tile * 16 + i) * (128 / w.group) + s * 32 / w.group;
+    const int groups = 128 / w.group, q = s * 32 / w.group, beside = w.beside();
+    return tile * 16 * groups + q / beside * 16 * beside + i * beside + q % beside;
   }
   // Whether this lane writes that scale, for its group.
   __device__ __forceinline__ bool writes(const Weights4& w, int s) const {

@@ -86,8 +86,7 @@ moe_status moe_norm_backward(moe_plan* plan, const moe_norm_config* cfg, const v
 /* ---- the experts' products with 4-bit weights -------------------------------- */
 
 typedef enum moe_weights4_format {
-  MOE_W4_INT4 = 0, /* w = scale * (code - 8), scale bf16, below 2^117 in magnitude, a scale per
-                      group of 32, 64 or 128                                                  */
+  MOE_W4_INT4 = 0, /* w = scale * (code - 8), scale bf16, a scale per group of 32, 64 or 128        */
   MOE_W4_E2M1 = 1  /* w = 2^(scale - 127) * OCP E2M1 value (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
                       negatives), scale E8M0 (255: NaN), a scale per group of 32              */
 } moe_weights4_format;
@@ -133,11 +132,14 @@ moe_status moe_weights4_unpack(const moe_weights4_config* cfg, const void* packe
  * every receive row r of expert e,
  *   z[r] = x[r] . w[e]^T + bias[e]        (float32 accumulation)
  *   y[r] = act(z[r]) + residual[r]        rounded to bf16 (nearest even)
- * E2M1 weights are multiplied as they are; so are INT4 weights where experts have
- * few rows, and where they have many as scale * (code - 8) rounded to bf16, the
- * type that the matrix cores take.  Arguments as moe_expert_linear; w4->experts, rows and in_features are the
- * plan's E and cfg's Z and K.  A row of x with an infinity or a NaN gives a
- * row that is not finite.
+ * No weight is rounded: E2M1 weights are bf16 numbers, and of INT4 weights the
+ * codes are multiplied, and a group's float32 sum by its scale.  (That sum is
+ * the difference of sums of products with 128 + code and with 136: it rounds as
+ * sums of their magnitude do, and x has to stay below 2^112.)  Arguments as
+ * moe_expert_linear; w4->experts, rows and in_features are the plan's E and
+ * cfg's Z and K.  A row of x with an infinity or a NaN gives a row that is not
+ * finite.  INT4 in groups of 32 is for batches of few rows an expert: large ones
+ * take two to three times as long as with groups of 64 or 128.
  * Errors: PLAN_NOT_ROUTED, INVALID_ARGUMENT, UNSUPPORTED (sizes beyond the
  * limits), HIP. */
 moe_status moe_expert_linear4(moe_plan* plan, const moe_expert_config* cfg,

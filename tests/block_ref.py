@@ -128,9 +128,7 @@ def quantize4(w, fmt, group):
 
 def expert_linear4(x, codes, scales, fmt, group, bias, residual, kind, off):
     """(y, bound of y).  The products of INT4 codes are added up as products with 128 + c and
-    with -136, so that their roundings are of sums of magnitude |x| (264 + c) times the scale.  Where
-    experts have many rows they are multiplied as scale * (c - 8) rounded to bf16 instead: each weight
-    moves by half a step at most."""
+    with -136, so that their roundings are of sums of magnitude |x| (264 + c) times the scale."""
     w, s = values4(codes, scales, fmt, group)
     rows, K = x.shape
     z = np.zeros((rows, w.shape[1]))
@@ -142,7 +140,6 @@ def expert_linear4(x, codes, scales, fmt, group, bias, residual, kind, off):
         e[a:b] = (K + 8) * 2 * U * mag
         if fmt == "int4":
             e[a:b] += (2 * group + 2) * 2 * U * (np.abs(x[a:b]) @ (np.abs(s[i]) * (264 + codes[i])).T)
-            e[a:b] += BF16_HALF * mag
         if bias is not None:
             z[a:b] += bias[i]
             e[a:b] += 2 * U * (np.abs(z[a:b]) + np.abs(bias[i]))

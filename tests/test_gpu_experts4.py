@@ -295,7 +295,6 @@ def test_block_step_by_step(T, kw, fmt, group, dev):
                 full[:, :K] = np.abs(w[e])
                 scale = np.repeat(full.reshape(-1, n, group).max(2) / 6.9, group, 1)[:, :K]
                 ez[a] += (2 * group + 2) * 2 * ref.U * 279 * (np.abs(f64(x)[a]) @ scale.T)
-                ez[a] += ref.BF16_HALF * (np.abs(f64(x)[a]) @ np.abs(w[e]).T)   # weights in bf16
         if act == "swiglu":
             n = z.shape[1] // 2
             y = ref.act(act, z[:, :n]) * z[:, n:]
