@@ -1,9 +1,9 @@
 """MI355X (gfx950) MoE expert-parallel shuffle.
 
 A thin binding over the C ABI of ``libmoeshuffle.so`` (include/moe_shuffle.h,
-include/moe_layer.h and include/moe_block.h): the same calls, with torch tensors for device memory and torch's current
-stream.  Every step of the shuffle runs in the library's HIP kernels; this
-module only checks shapes and passes pointers.
+include/moe_layer.h and include/moe_block.h): the same calls, with torch tensors
+for device memory and torch's current stream.  Every step of the shuffle runs in
+the library's HIP kernels; this module only checks shapes and passes pointers.
 
     plan = route_plan(topk_idx, num_experts=E, num_ranks=R, hidden=H,
                       ranks_per_node=G, node_dedup=False)
@@ -30,6 +30,15 @@ the layer's gradients:
     grad_recv, grad_w1, _ = expert_linear_backward(plan, grad_h, recv, w1, pre, "swiglu")
     grad_x = dispatch_backward(plan, grad_recv)
     grad_logits = router_backward(plan, logits, idx, grad_w)
+
+Before it stands the norm of the residual stream, and a model that only answers
+may keep its experts' weights in 4 bits:
+
+    h, stream, stats = norm(plan, x, gamma, residual=delta, save_stats=True)
+    grad_x, grad_gamma, _ = norm_backward(plan, grad_h, stream, stats, gamma)
+
+    w4 = quantize_experts4(w1, "int4", 128)     # once; pack_experts4 for a checkpoint's codes
+    h = expert_linear4(plan, recv, w4, activation="swiglu")
 
 Outputs may be given to these calls; they share no memory with other arguments.
 """

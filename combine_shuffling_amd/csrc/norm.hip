@@ -1,12 +1,23 @@
 // Layer norm and RMS norm of the residual stream's rows on gfx950, after the
 // residual addition, and their gradient.
+//   total = x + residual (rounded to x's type), h = (total - mean) rstd, y = h gamma + beta
+//   g = grad_y gamma, grad_x = rstd (g - mean(g) - h mean(g h)) + grad_total (RMS: no mean(g)),
+//   grad_gamma = sum of grad_y h over the rows, grad_beta = sum of grad_y
 //
 // Both are bound by HBM: a row is read once and kept in registers between the
-// statistics and the result.  A row belongs to W waves (or to 16 or 32 lanes of one, where it is
+// statistics and the result (the variance from the differences to the mean, not from the squares'
+// sum, which would cancel).  A row belongs to W waves (or to 16 or 32 lanes of one, where it is
 // narrow), 8 columns a lane and chunk; the statistics are folded over the lanes by
 // data-parallel moves and over the waves through LDS, in a fixed order.  Blocks
 // stay and take row after row, so that the weights are read once a block, and
-// a row's loads are under way while the row before it is reduced.
+// a row's loads are under way while the row before it is reduced.  Everything between load and store
+// is float32; the total is rounded before the statistics are taken, so that the gradient, which
+// reads it back, has the same ones.
+//
+// Measured: forward, 32768 x 2048 with residual and total, float32 to bf16: 178 us, 5.3 TB/s (with
+// streaming loads 200, with streaming stores 183); 16 x 7168: 4.1 us, a launch and a row's chain of
+// load, fold and store.  Gradient, 16384 x 7168 bf16 with all outputs: 176 us, 5.3 TB/s; 4099 x 1000:
+// 16.5 us with the sums' launch.
 #include <algorithm>
 #include <type_traits>
 
@@ -254,7 +265,10 @@ __global__ __launch_bounds__(kMaxWaves * kWave) void norm_kernel(
 }
 
 // Gradient: of the rows, and a block's sums of the weights' gradients (rows blockIdx.x of the
-// partial sums, or the sums themselves where there is one block).
+// partial sums, or the sums themselves where there is one block).  A lane adds up its columns over the
+// block's rows in registers, the block's rows at a time are joined once at the end (in one pass over
+// LDS), and the blocks' sums by norm_sum_kernel, in a fixed order and with no atomics: 256 rows of
+// partial sums cost 2% of the traffic of 16384 rows.
 template <bool XF32, bool YF32, int L, int CH>
 __global__ __launch_bounds__(kMaxWaves * kWave) void norm_grad_kernel(
     NormDims n, Spread s, const void* __restrict__ gy, const void* __restrict__ x,
@@ -451,6 +465,8 @@ hipError_t with_types(const NormDims& n, F f) {
 
 }  // namespace
 
+// Up to four turns of one block, a block does it all: 128 x 256 takes 9.0 us so and 7.8 with two launches
+// in a captured graph, 10.2 and 14.3 from a program, whose launches cost more than the turns.
 int norm_partials(const NormDims& n) {
   int threads;
   const Spread s = spread(n, kMaxWaves, &threads);

@@ -171,6 +171,8 @@ def test_products_of_integers_are_exact(T, E, k, K, N, kind, fmt, group, dev):
     (90, 5, 4, 2048, 4104, "skewed"),
     (300, 2, 2, 5000, 136, "uniform"),   # tiles
     (700, 200, 8, 136, 24, "few"),       # tiles of all rows on few of the experts
+    (4100, 5, 4, 264, 1032, "skewed"),   # E2M1: tiles of 128 rows
+    (4097, 3, 3, 1032, 1400, "uniform"),
 ])
 def test_long_and_odd_products_of_integers_are_exact(T, E, k, K, N, kind, fmt, group, dev):
     say(f"[experts4] exact, long T={T} E={E} k={k} K={K} N={N} {kind} {fmt} {group}")
