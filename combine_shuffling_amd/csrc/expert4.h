@@ -415,32 +415,41 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void expert4_few_rows_kernel(
 //
 // INT4: no weight is rounded.  A group's products with 128 + c are added up in sums of their own,
 // which start from its products with -136 and so come to those with c - 8, and the scale multiplies
-// the finished sums into the accumulators.  A wave takes 16 rows x 64 columns at a time through a
-// group, whose fragments it has expanded, so that the sums take 16 registers; tiles of 64 rows leave
-// room for them.  With 128 rows registers run out (425 us for 64 experts, top-8, 4096 tokens, 2048 ->
-// 2 x 1024, against 332), and with groups of 32, whose scales take a quarter of the registers, they
-// do with 64 rows too (3200 us; the kernel for few rows takes 740).
+// the finished sums into the accumulators.  The products with -136 are the same for all columns: each
+// of the four waves computes them for a quarter of the rows, of the next block, and leaves them in
+// LDS (with each computing all of them: 591 us against 580 for 8 experts, top-2, 8192 tokens, 4096 ->
+// 4096).  A wave takes 16 rows x 64 columns at a time through a group, whose fragments it has
+// expanded, so that the sums take 16 registers; tiles of 64 rows leave room for them.  With 128 rows
+// registers run out (425 us for 64 experts, top-8, 4096 tokens, 2048 -> 2 x 1024, against 355), and
+// with groups of 32, whose scales take a quarter of the registers, they do with 64 rows too (3200 us;
+// the kernel for few rows takes 740).  Without a branch after every 16 rows the scaling of one 16 runs
+// under the products of the next: 332 us and 537 for the two, but 43 against 41 for 256 tokens of the
+// first, which is for experts of 96 rows and more on average, and for groups of 128 (of 64: registers
+// run out).
 //
 // E2M1 weights are bf16 numbers, scale and all.  Tiles of 128 rows where there are four a CU: 252 us
-// for that example, 439 for 8 experts, top-2, 8192 tokens, 4096 -> 4096, against 314 and 514 with 64
-// rows, which leave fewer products for each weight that is expanded; where there are fewer tiles, 64
-// rows: 68 us against 82 for 512 tokens of the latter, 27 against 33 for 1021 tokens, top-4 of 30, 776
-// -> 1000.
+// for the 4096 tokens, 439 for the 8192, against 314 and 514 with 64 rows, which leave fewer products
+// for each weight that is expanded; where there are fewer tiles, 64 rows: 68 us against 82 for 512
+// tokens of the latter, 27 against 33 for 1021 tokens, top-4 of 30, 776 -> 1000.
 //
-// What bounds the large products: the matrix cores are busy half of the time; expanding codes and
-// scaling sums take as many cycles of the vector units, which two waves a SIMD overlap in part.
-template <int G, bool E2M1, bool GATED_, int MI_>
+// What bounds the large products: with INT4 the matrix cores are busy in 40% of the cycles and the
+// vector units, which expand codes and scale sums, in as many, and little of the one runs under the
+// other; a SIMD has room for two waves.
+template <int G, bool E2M1, bool GATED_, int MI_, bool SKIP>
 struct Tile4 {
   static constexpr int WM = 1, WN = 4, MI = MI_, BM = MI * 16, BN = 256, NJ = 4;
   static constexpr bool GATED = GATED_;
   static constexpr int kNW = WM * WN, kThreads = kNW * kWave;
-  static constexpr int kStage = BM * 256, kStages = MI == 8 ? 2 : 3, kLds = kStages * kStage;
+  static constexpr int kStage = BM * 256, kStages = MI == 8 ? 2 : E2M1 ? 3 : 4;
   static constexpr int kAhead = kStages - 1;      // blocks of x that are under way
   static constexpr int QA = kStage / 1024 / kNW;  // loads of x a wave and block
   static constexpr int kGroups = 128 / G;         // groups of a row and block
   static constexpr int kSteps = G / 32;           // matrix instructions a group and fragment
   static constexpr int kBlocksACu = E2M1 && GATED && MI == 4 ? 3 : 2;
   static constexpr int m0 = 0;  // every wave has all the rows of the tile
+  // INT4: a block's products with -136, [group][row] (four times each), of this block and the next.
+  static constexpr int kLess = E2M1 ? 0 : kGroups * BM * 16;
+  static constexpr int kLds = kStages * kStage + 2 * kLess;
 
   // Codes of a block of 128 of the wave's columns, and the scales of the lane's results.
   struct Packed {
@@ -462,13 +471,15 @@ struct Tile4 {
   uint32_t va;       // byte offset of this lane's first load of a block of x
   uint32_t from_[4]; // byte offsets of the lane's fragments s of the first 16 rows of a stage
   int put;           // LDS offset of the stage that is read next
+  int less;          // and of its products with -136
   bf16x8 offset;
 
   __device__ __forceinline__ Tile4(const ExpertDims& d, const Weights4& w4, const char* x_,
                                       const char* codes_, const char* scales_)
       : x(x_), codes(codes_), scales(scales_), lda((uint32_t)d.K * 2), codes_stride(w4.codes_stride()),
         scales_stride(w4.scales_stride()), codes_bytes(w4.tiles * w4.codes_stride()),
-        scales_bytes(w4.tiles * w4.scales_stride()), K(d.K), blocks(w4.blocks), second(d.N), put(0) {
+        scales_bytes(w4.tiles * w4.scales_stride()), K(d.K), blocks(w4.blocks), second(d.N), put(0),
+        less(kStages * kStage) {
     lane = threadIdx.x % kWave;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int i = lane & 15, g = lane >> 4;
@@ -546,13 +557,30 @@ struct Tile4 {
     __builtin_amdgcn_sched_barrier(0);
   }
 
+  // Products with -136 of the wave's quarter of the rows of x at `from`, to `to`.
+  __device__ __forceinline__ void products_less(const char* __restrict__ from,
+                                                char* __restrict__ to) const {
+    static_assert(E2M1 || MI == kNW);
+#pragma unroll
+    for (int q = 0; q < kGroups; ++q) {
+      f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+        t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            offset,
+            *reinterpret_cast<const bf16x8*>(from + wave * 4096 + from_[q * kSteps + s]), t, 0, 0, 0);
+      if (lane < 16) *reinterpret_cast<f32x4*>(to + (q * BM + wave * 16 + lane) * 16) = t;
+    }
+  }
+
   // Products of a block with x at `from`, under the loads of x kAhead blocks on (wx), to another
   // stage, which saying so (restrict) keeps the reads from waiting for, and those of the next block's
   // codes and scales (wp), which take the place of this block's: the scales when all are used, which
-  // saves registers.  rows: rows of the tile that there are (products of 16 rows that are all absent
-  // are skipped).
+  // saves registers.  rows: rows of the tile that there are (SKIP: products of 16 rows that are all
+  // absent are left out).
   __device__ __forceinline__ void multiply(const Walk& wx, const Walk& wp, char* __restrict__ to,
-                                           const char* __restrict__ from, int rows, Packed& p) {
+                                           const char* __restrict__ from, const char* __restrict__ less,
+                                           int rows, Packed& p) {
     u32x4 then[NJ];
     load_codes(then, wp);
     load_x(wx, to);
@@ -568,7 +596,7 @@ struct Tile4 {
           b[j] = decode_e2m1(p.codes[j][s], e2m1_scale((p.scales[j] >> (8 * s)) & 0xffu));
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-          if (i > 0 && rows <= i * 16) break;
+          if (SKIP && i > 0 && rows <= i * 16) break;
           const bf16x8 a = fragment(i, s);
 #pragma unroll
           for (int j = 0; j < NJ; ++j)
@@ -589,19 +617,18 @@ struct Tile4 {
         }
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-          if (i > 0 && rows <= i * 16) break;
-          f32x4 less = {0.0f, 0.0f, 0.0f, 0.0f}, part[NJ];
+          if (SKIP && i > 0 && rows <= i * 16) break;
+          const f32x4 start =
+              *reinterpret_cast<const f32x4*>(less + (q * BM + i * 16 + (lane & 15)) * 16);
+          f32x4 part[NJ];
           bf16x8 a[kSteps];
 #pragma unroll
-          for (int s = 0; s < kSteps; ++s) {
-            a[s] = fragment(i, q * kSteps + s);
-            less = __builtin_amdgcn_mfma_f32_16x16x32_bf16(offset, a[s], less, 0, 0, 0);
-          }
+          for (int s = 0; s < kSteps; ++s) a[s] = fragment(i, q * kSteps + s);
 #pragma unroll
           for (int s = 0; s < kSteps; ++s)
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
-              part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[s][j], a[s], s == 0 ? less : part[j],
+              part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[s][j], a[s], s == 0 ? start : part[j],
                                                                 0, 0, 0);
 #pragma unroll
           for (int j = 0; j < NJ; ++j)
@@ -629,14 +656,18 @@ struct Tile4 {
       for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     for (int n = 0; n < blocks; ++n) {
       // A tile's first kAhead blocks of x had landed before the last epilogue.  After a later one's
-      // loads came scales, and those of a whole block where two are under way.
-      if (n < kAhead)
+      // loads came scales, and those of a whole block where more are under way than are needed now:
+      // this block, and with INT4 the next.
+      if (n + (E2M1 ? 0 : 1) < kAhead)
         wait_and_meet<-1>();
       else
         wait_and_meet<kAhead == 1 ? NJ : NJ + QA + 2 * NJ>();
-      const int next = stage_after(put);
-      multiply(wx, wp, lds + (kAhead == 1 ? next : stage_after(next)), lds + put, rows, now);
+      const int next = stage_after(put), other = 2 * kStages * kStage + kLess - less;
+      const int free = put == 0 ? (kStages - 1) * kStage : put - kStage;
+      if constexpr (!E2M1) products_less(lds + next, lds + other);
+      multiply(wx, wp, lds + free, lds + put, lds + less, rows, now);
       put = next;
+      less = other;
       advance(wx);
       advance(wp);
     }
@@ -714,6 +745,10 @@ __global__ __launch_bounds__(P::kThreads, P::kBlocksACu) void expert4_rows_kerne
     advance(wx);
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  if constexpr (P::kLess > 0) {
+    P::template wait_and_meet<-1>();
+    p.products_less(lds, lds + p.less);
+  }
   while (w.s.rows > 0) {
     p.run(lds, wx, wp, advance, w.s.rows, packed);
     tile4_epilogue(p, x, w.s, w.n0, bias, residual, y);
@@ -789,12 +824,17 @@ hipError_t expert_rows4(const ExpertDims& x, const Weights4& w4, const int32_t* 
     }
     if constexpr (E2M1) {
       if ((int64_t)x.rows * ceil_div(x.N, gated(x.act) ? 128 : 256) >= 128 * 4 * kCus)
-        return gated(x.act) ? tiles(Type<Tile4<G, E2M1, true, 8>>())
-                            : tiles(Type<Tile4<G, E2M1, false, 8>>());
+        return gated(x.act) ? tiles(Type<Tile4<G, E2M1, true, 8, true>>())
+                            : tiles(Type<Tile4<G, E2M1, false, 8, true>>());
+    }
+    if constexpr (!E2M1 && G == 128) {
+      if ((int64_t)x.rows >= (int64_t)x.E * 96)
+        return gated(x.act) ? tiles(Type<Tile4<G, E2M1, true, 4, false>>())
+                            : tiles(Type<Tile4<G, E2M1, false, 4, false>>());
     }
     if constexpr (E2M1 || G > 32)
-      return gated(x.act) ? tiles(Type<Tile4<G, E2M1, true, 4>>())
-                          : tiles(Type<Tile4<G, E2M1, false, 4>>());
+      return gated(x.act) ? tiles(Type<Tile4<G, E2M1, true, 4, true>>())
+                          : tiles(Type<Tile4<G, E2M1, false, 4, true>>());
     else
       return hipErrorInvalidValue;  // (few4 takes them all)
   };
