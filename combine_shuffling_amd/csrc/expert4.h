@@ -427,10 +427,11 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void expert4_few_rows_kernel(
 // first, which is for experts of 96 rows and more on average, and for groups of 128 (of 64: registers
 // run out).
 //
-// E2M1 weights are bf16 numbers, scale and all.  Tiles of 128 rows where there are four a CU: 252 us
-// for the 4096 tokens, 439 for the 8192, against 314 and 514 with 64 rows, which leave fewer products
-// for each weight that is expanded; where there are fewer tiles, 64 rows: 68 us against 82 for 512
-// tokens of the latter, 27 against 33 for 1021 tokens, top-4 of 30, 776 -> 1000.
+// E2M1 weights are bf16 numbers, scale and all.  Tiles of 128 rows where there are four a CU and
+// experts have that many: 253 us for the 4096 tokens, 450 for the 8192 (266 and 464 with branches),
+// against 314 and 514 with 64 rows, which leave fewer products for each weight that is expanded; where
+// there are fewer tiles, 64 rows: 68 us against 82 for 512 tokens of the latter, 27 against 33 for
+// 1021 tokens, top-4 of 30, 776 -> 1000.
 //
 // What bounds the large products: with INT4 the matrix cores are busy in 40% of the cycles and the
 // vector units, which expand codes and scale sums, in as many, and little of the one runs under the
@@ -822,13 +823,13 @@ hipError_t expert_rows4(const ExpertDims& x, const Weights4& w4, const int32_t* 
       if (x.T <= 16 || (int64_t)x.rows <= (int64_t)x.E * 12) return few(std::integral_constant<int, 1>());
       return few(std::integral_constant<int, 2>());
     }
+    const bool whole = (int64_t)x.rows >= (int64_t)x.E * 96;  // most tiles have all of their rows
     if constexpr (E2M1) {
-      if ((int64_t)x.rows * ceil_div(x.N, gated(x.act) ? 128 : 256) >= 128 * 4 * kCus)
-        return gated(x.act) ? tiles(Type<Tile4<G, E2M1, true, 8, true>>())
-                            : tiles(Type<Tile4<G, E2M1, false, 8, true>>());
-    }
-    if constexpr (!E2M1 && G == 128) {
-      if ((int64_t)x.rows >= (int64_t)x.E * 96)
+      if (whole && (int64_t)x.rows * ceil_div(x.N, gated(x.act) ? 128 : 256) >= 128 * 4 * kCus)
+        return gated(x.act) ? tiles(Type<Tile4<G, E2M1, true, 8, false>>())
+                            : tiles(Type<Tile4<G, E2M1, false, 8, false>>());
+    } else if constexpr (G == 128) {
+      if (whole)
         return gated(x.act) ? tiles(Type<Tile4<G, E2M1, true, 4, false>>())
                             : tiles(Type<Tile4<G, E2M1, false, 4, false>>());
     }

@@ -173,6 +173,7 @@ def test_products_of_integers_are_exact(T, E, k, K, N, kind, fmt, group, dev):
     (700, 200, 8, 136, 24, "few"),       # tiles of all rows on few of the experts
     (4100, 5, 4, 264, 1032, "skewed"),   # E2M1: tiles of 128 rows
     (4097, 3, 3, 1032, 1400, "uniform"),
+    (1500, 200, 8, 136, 1400, "uniform"),  # as many tiles, but few rows an expert
 ])
 def test_long_and_odd_products_of_integers_are_exact(T, E, k, K, N, kind, fmt, group, dev):
     say(f"[experts4] exact, long T={T} E={E} k={k} K={K} N={N} {kind} {fmt} {group}")
