@@ -37,8 +37,8 @@ hipError_t launch_norm_grad(const NormDims& n, const void* gy, const void* total
 // them).  Lane 16 g + i has row i, and in word s of its four the weights 32 s + 8 g + 0..7, which
 // are what it multiplies in the tile's matrix instruction s of 32 weights.  In a word E2M1 weight
 // j is nibble j, as the conversion instruction takes them; INT4 weight 2p is nibble p and weight
-// 2p + 1 nibble p + 4, so that one shift and one mask leave a pair of them in the halves of a
-// register.
+// 2p + 1 nibble p + 4 of a word that is then rotated left by 3, so that one rotation by 4p and one mask
+// leave a pair of them as the upper mantissa bits of the bf16 numbers in the halves of a register.
 // Scales follow at a multiple of 256 bytes, tile by tile in the same order, so that a lane finds those
 // of its row (E2M1, bytes: [16 rows][4 groups]), or of the four consecutive rows that its results are
 // (INT4, bf16: [16 rows], [16 rows][2 groups], or two of these with groups of 32), side by side.

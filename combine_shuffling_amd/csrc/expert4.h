@@ -23,15 +23,18 @@ __device__ __forceinline__ bf16x8 decode_e2m1(uint32_t codes, float scale) {
 
 __device__ __forceinline__ float e2m1_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// Eight INT4 codes c (0..15) as the bf16 numbers 128 + c: the code is the low bits of the mantissa
-// under the exponent of 128.
-constexpr float kInt4Offset = 136.0f;  // 128 + c stands for c - 8
+// Eight INT4 codes c (0..15) as the bf16 numbers 16 + c: the code is the upper four bits of the mantissa
+// under the exponent of 16.  (As the lower four, under that of 128, a group's sums are of six times the
+// magnitude, and lose that much more to rounding.)  One rotation and one mask with the exponent for a
+// pair, none for the first.
+constexpr float kInt4Offset = 24.0f;  // 16 + c stands for c - 8
 __device__ __forceinline__ bf16x8 decode_int4(uint32_t codes) {
-  uint32_t magic = 0x43004300u;
+  uint32_t magic = 0x41804180u;
   asm("" : "+v"(magic));  // in a vector register: an instruction takes one constant of another kind
   u32x4 r;
 #pragma unroll
-  for (int p = 0; p < 4; ++p) r[p] = ((codes >> (4 * p)) & 0x000f000fu) | magic;
+  for (int p = 0; p < 4; ++p)
+    r[p] = (__builtin_rotateright32(codes, 4 * p) & 0x00780078u) | magic;
   return __builtin_bit_cast(bf16x8, r);
 }
 
@@ -103,8 +106,8 @@ struct Int4Scales {
 // strip: it loads codes and scales straight into registers, 1024 consecutive bytes a load, one
 // step of U blocks of 128 ahead of the one that it multiplies.
 //
-// E2M1 weights are exact in bf16, scale and all.  INT4: the sums of a group's products with 128 + c
-// and with -136 are added up in float32, which leaves the sum with c - 8, and the scale multiplies
+// E2M1 weights are exact in bf16, scale and all.  INT4: the sums of a group's products with 16 + c
+// and with -24 are added up in float32, which leaves the sum with c - 8, and the scale multiplies
 // that sum: no weight is rounded.
 //
 // Bound by HBM.  16 tokens, top-8 of 64, 2048 -> 2 x 1024, E2M1: 26 us, 5 TB/s of codes and scales; of
@@ -413,9 +416,9 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void expert4_few_rows_kernel(
 // contraction ahead (a fourth of what bf16 takes), and turns eight codes a lane and fragment into
 // bf16 while another block's products run.
 //
-// INT4: no weight is rounded.  A group's products with 128 + c are added up in sums of their own,
-// which start from its products with -136 and so come to those with c - 8, and the scale multiplies
-// the finished sums into the accumulators.  The products with -136 are the same for all columns: each
+// INT4: no weight is rounded.  A group's products with 16 + c are added up in sums of their own,
+// which start from its products with -24 and so come to those with c - 8, and the scale multiplies
+// the finished sums into the accumulators.  The products with -24 are the same for all columns: each
 // of the four waves computes them for a quarter of the rows, of the next block, and leaves them in
 // LDS (with each computing all of them: 591 us against 580 for 8 experts, top-2, 8192 tokens, 4096 ->
 // 4096).  A wave takes 16 rows x 64 columns at a time through a group, whose fragments it has
@@ -448,7 +451,7 @@ struct Tile4 {
   static constexpr int kSteps = G / 32;           // matrix instructions a group and fragment
   static constexpr int kBlocksACu = E2M1 && GATED && MI == 4 ? 3 : 2;
   static constexpr int m0 = 0;  // every wave has all the rows of the tile
-  // INT4: a block's products with -136, [group][row] (four times each), of this block and the next.
+  // INT4: a block's products with -24, [group][row] (four times each), of this block and the next.
   static constexpr int kLess = E2M1 ? 0 : kGroups * BM * 16;
   static constexpr int kLds = kStages * kStage + 2 * kLess;
 
@@ -472,7 +475,7 @@ struct Tile4 {
   uint32_t va;       // byte offset of this lane's first load of a block of x
   uint32_t from_[4]; // byte offsets of the lane's fragments s of the first 16 rows of a stage
   int put;           // LDS offset of the stage that is read next
-  int less;          // and of its products with -136
+  int less;          // and of its products with -24
   bf16x8 offset;
 
   __device__ __forceinline__ Tile4(const ExpertDims& d, const Weights4& w4, const char* x_,
@@ -558,7 +561,7 @@ struct Tile4 {
     __builtin_amdgcn_sched_barrier(0);
   }
 
-  // Products with -136 of the wave's quarter of the rows of x at `from`, to `to`.
+  // Products with -24 of the wave's quarter of the rows of x at `from`, to `to`.
   __device__ __forceinline__ void products_less(const char* __restrict__ from,
                                                 char* __restrict__ to) const {
     static_assert(E2M1 || MI == kNW);

@@ -61,10 +61,11 @@ __device__ __forceinline__ uint32_t int4_word(uint32_t v) {
   uint32_t r = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) r |= ((v >> (4 * i)) & 15u) << (4 * (i / 2) + 16 * (i % 2));
-  return r;
+  return __builtin_rotateleft32(r, 3);
 }
 __device__ __forceinline__ uint32_t int4_nibbles(uint32_t v) {
   uint32_t r = 0;
+  v = __builtin_rotateright32(v, 3);
 #pragma unroll
   for (int i = 0; i < 8; ++i) r |= ((v >> (4 * (i / 2) + 16 * (i % 2))) & 15u) << (4 * i);
   return r;
@@ -79,7 +80,7 @@ __device__ __forceinline__ void put_scale(const Weights4& w, const At& at, int s
     static_cast<uint16_t*>(scales)[at.scale(w, s)] = (uint16_t)scale;
 }
 
-// What pads rows and K: weights of 0 under a finite scale.
+// What pads rows and K: weights of 0 under a finite scale (codes in a checkpoint's order).
 __device__ __forceinline__ uint32_t pad_codes(const Weights4& w) { return w.e2m1 ? 0u : 0x88888888u; }
 __device__ __forceinline__ uint32_t pad_scale(const Weights4& w) { return w.e2m1 ? 127u : 0u; }
 
@@ -175,7 +176,8 @@ __global__ __launch_bounds__(kThreads) void quantize4_kernel(Weights4 w,
       }
     }
     const bool in = at.in_rows && at.k(s) < w.K;
-    piece[s] = !in ? pad_codes(w) : w.e2m1 ? codes : int4_word(codes);
+    if (!in) codes = pad_codes(w);
+    piece[s] = w.e2m1 ? codes : int4_word(codes);
     put_scale(w, at, s, at.in_rows && at.k0 + 32 * s < w.K ? scale : pad_scale(w), scales);
   }
   pieces[at.piece] = piece;
