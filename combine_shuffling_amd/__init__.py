@@ -162,14 +162,14 @@ def _run(name: str, device: torch.device, *args) -> None:
 
 class ExpertWeights4:
     """Expert weights [experts, rows, in_features] in 4 bits, packed for expert_linear4: made by
-    pack_experts4 or quantize_experts4.  packed: the buffer (uint8)."""
+    pack_experts4 or quantize_experts4.  packed: the buffer (uint8); one that was saved may take its
+    place, in weights of the same sizes, format and group."""
 
     def __init__(self, experts: int, rows: int, in_features: int, format: str, group: int,
                  device: torch.device):
         if format not in _abi.WEIGHTS4:
             raise ValueError(f"format must be one of {tuple(_abi.WEIGHTS4)}")
-        self.experts, self.rows, self.in_features = experts, rows, in_features
-        self.format, self.group, self.device = format, group, device
+        self.format, self.group = format, group
         self._cfg = _abi.Weights4Config(experts, rows, in_features, _abi.WEIGHTS4[format], group)
         self.cfg = ctypes.byref(self._cfg)
         size = _abi.lib().moe_weights4_bytes(self.cfg)
@@ -177,6 +177,15 @@ class ExpertWeights4:
             raise ValueError(f"{format} weights of {experts} x {rows} x {in_features} in groups of "
                              f"{group} are not supported")
         self.packed = torch.empty(size, dtype=torch.uint8, device=device)
+        self.device, self._size = self.packed.device, (size,)
+
+    experts = property(lambda self: self._cfg.experts)
+    rows = property(lambda self: self._cfg.rows)
+    in_features = property(lambda self: self._cfg.in_features)
+
+    def check(self, device: torch.device) -> None:
+        """The library reads packed as long as the sizes say."""
+        _need(self.packed, self._size, (torch.uint8,), "packed", device)
 
     def values(self, dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
         """moe_weights4_unpack: the values that the weights stand for, [experts, rows,
@@ -189,6 +198,7 @@ class ExpertWeights4:
 @_on_stream
 def _values4(w4: ExpertWeights4, dtype: torch.dtype) -> torch.Tensor:
     code = _out_code(dtype, "dtype")
+    w4.check(w4.device)
     w = torch.empty((w4.experts, w4.rows, w4.in_features), dtype=dtype, device=w4.device)
     _run("moe_weights4_unpack", w4.device, w4.cfg,
          w4.packed.data_ptr(), w.data_ptr(), code)
@@ -686,7 +696,7 @@ class Plan:
                 raise ValueError("a gated activation needs halves of a multiple of 8 weight rows")
             N = Z // 2
         rows = self.recv_rows
-        _need(w4.packed, w4.packed.shape, (torch.uint8,), "w4", dev)
+        w4.check(dev)
         _need(x, (rows, K), _BF16, "x", dev)
         if bias is not None:
             _need(bias, (self.E, Z), _F32, "bias", dev)
