@@ -132,14 +132,15 @@ moe_status moe_weights4_unpack(const moe_weights4_config* cfg, const void* packe
  * every receive row r of expert e,
  *   z[r] = x[r] . w[e]^T + bias[e]        (float32 accumulation)
  *   y[r] = act(z[r]) + residual[r]        rounded to bf16 (nearest even)
- * No weight is rounded: E2M1 weights are bf16 numbers, and of INT4 weights the
- * codes are multiplied, and a group's float32 sum by its scale.  (That sum is
- * the difference of sums of products with 16 + code and with 24: it rounds as
- * sums of their magnitude do, and x has to stay below 2^116.)  Arguments as
- * moe_expert_linear; w4->experts, rows and in_features are the plan's E and
- * cfg's Z and K.  A row of x with an infinity or a NaN gives a row that is not
- * finite.  INT4 in groups of 32 is for batches of few rows an expert: large ones
- * take two to three times as long as with groups of 64 or 128.
+ * No weight is rounded: E2M1 weights are bf16 numbers, subnormal ones too (and
+ * infinite from 2^128 on), and of INT4 weights the codes are multiplied, and a
+ * group's float32 sum by its scale.  (That sum is the difference of sums of
+ * products with 16 + code and with 24: it rounds as sums of their magnitude do,
+ * and x has to stay below 2^116.)  Arguments as moe_expert_linear; w4->experts,
+ * rows and in_features are the plan's E and cfg's Z and K.  A row of x with an
+ * infinity or a NaN gives a row that is not finite.  INT4 in groups of 32 is for
+ * batches of few rows an expert: large ones take two to three times as long as
+ * with groups of 64 or 128.
  * Errors: PLAN_NOT_ROUTED, INVALID_ARGUMENT, UNSUPPORTED (sizes beyond the
  * limits), HIP. */
 moe_status moe_expert_linear4(moe_plan* plan, const moe_expert_config* cfg,
