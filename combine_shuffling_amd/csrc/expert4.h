@@ -449,7 +449,6 @@ struct Tile4 {
   static constexpr int QA = kStage / 1024 / kNW;  // loads of x a wave and block
   static constexpr int kGroups = 128 / G;         // groups of a row and block
   static constexpr int kSteps = G / 32;           // matrix instructions a group and fragment
-  static constexpr int kBlocksACu = E2M1 && GATED && MI == 4 ? 3 : 2;
   static constexpr int m0 = 0;  // every wave has all the rows of the tile
   // INT4: a block's products with -24, [group][row] (four times each), of this block and the next.
   static constexpr int kLess = E2M1 ? 0 : kGroups * BM * 16;
@@ -711,7 +710,7 @@ __device__ __forceinline__ void tile4_epilogue(const P& p, const ExpertDims& x, 
 }
 
 template <typename P>
-__global__ __launch_bounds__(P::kThreads, P::kBlocksACu) void expert4_rows_kernel(
+__global__ __launch_bounds__(P::kThreads, 2) void expert4_rows_kernel(
     ExpertDims x, Weights4 w4, const int32_t* __restrict__ off, const char* __restrict__ a,
     const char* __restrict__ codes, const char* __restrict__ scales, const float* __restrict__ bias,
     const uint16_t* __restrict__ residual, uint16_t* __restrict__ y, int ntiles) {
