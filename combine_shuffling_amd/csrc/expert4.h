@@ -789,10 +789,13 @@ hipError_t expert_rows4(const ExpertDims& x, const Weights4& w4, const int32_t* 
       FewSplit cut{};
       cut.rows = MT * 16;
       if (MT == 1) {
-        // Fewer rows at a time where the contraction is too long for 16 and experts have few.
-        const int wanted = 2 * ceil_div(x.rows, x.E) + 2;
-        while (cut.rows > 4 && cut.rows * w4.blocks * 256 > F::kXBytes &&
-               (cut.rows / 2 >= x.T || cut.rows / 2 >= wanted))
+        // Fewer rows at a time where the contraction is too long for 16 and no expert can have more (top-8
+        // of 256, 7168 -> 2 x 1024, INT4 in groups of 128: 4 tokens take 46 us in passes of 4, 48 of 16).
+        // Not where the average alone is small, since an expert's passes follow one another: 16 tokens
+        // take 150 and 148 us, but 162 and 67 under Zipf 1.2, whose busiest expert has 16 rows; 500 tokens,
+        // top-1 of 1024, 7168 -> 128: 43 and 44, 1178 and 467 under Zipf; at worst, 16 tokens, top-1 of 128,
+        // 7168 -> 2048: 26 and 29, 47 and 27 under Zipf.
+        while (cut.rows > 4 && cut.rows * w4.blocks * 256 > F::kXBytes && cut.rows / 2 >= x.T)
           cut.rows /= 2;
       }
       cut.phase = std::min(w4.blocks, F::kXBytes / (cut.rows * 256));
