@@ -110,10 +110,16 @@ struct Int4Scales {
 // and with -24 are added up in float32, which leaves the sum with c - 8, and the scale multiplies
 // that sum: no weight is rounded.
 //
-// Bound by HBM.  16 tokens, top-8 of 64, 2048 -> 2 x 1024, E2M1: 26 us, 5 TB/s of codes and scales; of
-// 256 experts, 7168 -> 2 x 1024, INT4 in groups of 128: 149 us, 5.2 TB/s; one token of the former 7.4 us,
-// a launch and the chain offsets -> codes -> products -> join.  x in registers instead of LDS spilled
-// and halved the waves; several strips a wave, one after another, and passes of 64 rows were slower.
+// Bound by HBM.  16 tokens, top-8 of 64, 2048 -> 2 x 1024, E2M1: 26 us, 5 TB/s of codes and scales (INT4
+// in groups of 128, 64 and 32: 30, 33, 34); of 256 experts, 7168 -> 2 x 1024, INT4 in groups of 128: 149
+// us, 5.2 TB/s (64 and 32: 170, 193); one token of the former 7.4 us, a launch and the chain offsets ->
+// codes -> products -> join.  x in registers instead of LDS spilled and halved the waves; several
+// strips a wave, one after another, and passes of 64 rows were slower.  For 16 rows and groups of 64
+// and 32 some registers spill: 8 and 16 bytes of scratch a lane, 36 and 40 with a gate.
+//
+// Skewed routing: a busy expert's passes follow one another in its blocks.  190 tokens, top-8 of 256,
+// 2048 -> 2 x 1024, take 117 us with uniform routing (13 rows at most) and 143 under Zipf 1.2 with 0.7 of
+// the weights (186 rows: twelve passes).
 template <int G, bool E2M1, int MT>
 struct FewRows {
   static constexpr int kGroups = 128 / G;  // scales of a row and block
@@ -414,7 +420,7 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void expert4_few_rows_kernel(
 // x goes straight to LDS, in stages of 128 along the contraction.  The weights do not pass through
 // LDS: a wave loads the codes of its own 64 columns into registers, a block of 128 along the
 // contraction ahead (a fourth of what bf16 takes), and turns eight codes a lane and fragment into
-// bf16 while another block's products run.
+// bf16 between the products; what runs beside them is the other block of the CU.
 //
 // INT4: no weight is rounded.  A group's products with 16 + c are added up in sums of their own,
 // which start from its products with -24 and so come to those with c - 8, and the scale multiplies
@@ -438,7 +444,12 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void expert4_few_rows_kernel(
 //
 // What bounds the large products: with INT4 the matrix cores are busy in 40% of the cycles and the
 // vector units, which expand codes and scale sums, in as many, and little of the one runs under the
-// other; a SIMD has room for two waves.
+// other; a SIMD has room for two waves.  The loads take their part: the compiler issues those of the
+// next codes and of x at the end of a block's products where they have no branches (after 112 of 128
+// matrix instructions in E2M1 tiles of 128 rows, 50 to 54 of 64 in INT4 ones), and ahead of them where
+// they have; and in INT4 tiles it waits for all of them before it reads x for the products with -24,
+// since it cannot tell the stages of LDS apart, so that of the blocks of x under way (kAhead) the
+// next one's latency shows.
 template <int G, bool E2M1, bool GATED_, int MI_, bool SKIP>
 struct Tile4 {
   static constexpr int WM = 1, WN = 4, MI = MI_, BM = MI * 16, BN = 256, NJ = 4;
@@ -576,11 +587,11 @@ struct Tile4 {
     }
   }
 
-  // Products of a block with x at `from`, under the loads of x kAhead blocks on (wx), to another
-  // stage, which saying so (restrict) keeps the reads from waiting for, and those of the next block's
-  // codes and scales (wp), which take the place of this block's: the scales when all are used, which
-  // saves registers.  rows: rows of the tile that there are (SKIP: products of 16 rows that are all
-  // absent are left out).
+  // Products of a block with x at `from`, the loads of x kAhead blocks on (wx), to another stage, which
+  // saying so (restrict) keeps these reads from waiting for, and those of the next block's codes and
+  // scales (wp), which take the place of this block's: the scales when all are used, which saves
+  // registers.  rows: rows of the tile that there are (SKIP: products of 16 rows that are all absent
+  // are left out).
   __device__ __forceinline__ void multiply(const Walk& wx, const Walk& wp, char* __restrict__ to,
                                            const char* __restrict__ from, const char* __restrict__ less,
                                            int rows, Packed& p) {
@@ -761,7 +772,8 @@ __global__ __launch_bounds__(P::kThreads, 2) void expert4_rows_kernel(
 
 // The kernel for few rows is taken up to 6 rows an expert on average, up to 80 where the tiles would
 // leave half of the CUs without one, and always with INT4 in groups of 32 (Tile4).  Its passes take
-// 16 rows where no expert has more or they have up to 12 on average, else 32.  In us, passes of 16, of
+// 16 rows where no expert has more or they have up to 12 on average, else 32.  (All by the average, which
+// the host has; measured with uniform routing.)  In us, passes of 16, of
 // 32, and tiles of 64 rows, INT4 in groups of 128 (E2M1): 64 experts, top-8, 2048 -> 2 x 1024: 8 tokens
 // 22, 30, 28 (20, 24, 27), 48 tokens 28, 36, 31 (27, 33, 30), 64 tokens 33, 38, 30 (31, 32, 29), 256
 // tokens 69, 67, 40 (67, 55, 37); 30 experts, top-2, 4096 -> 4096: 32 tokens 48, 63, 52 (46, 55, 50), 64

@@ -16,8 +16,8 @@
 //
 // Measured: forward, 32768 x 2048 with residual and total, float32 to bf16: 178 us, 5.3 TB/s (with
 // streaming loads 200, with streaming stores 183); 16 x 7168: 4.1 us, a launch and a row's chain of
-// load, fold and store.  Gradient, 16384 x 7168 bf16 with all outputs: 176 us, 5.3 TB/s; 4099 x 1000:
-// 16.5 us with the sums' launch.
+// load, fold and store; 16384 x 16384 bf16: 404 us, 5.3 TB/s.  Gradient, 16384 x 7168 bf16 with all
+// outputs: 176 us, 5.3 TB/s; 16384 x 16384: 469 us, 4.6 TB/s; 4099 x 1000: 16.5 us with the sums' launch.
 #include <algorithm>
 #include <type_traits>
 
@@ -286,7 +286,8 @@ __global__ __launch_bounds__(kMaxWaves * kWave) void norm_grad_kernel(
     for (int q = 0; q < 8; ++q) sg[i][q] = sb[i][q] = 0.0f;
   }
   // With two chunks a lane there are no registers for the loads of a row ahead, and gtotal is
-  // loaded where it is added.
+  // loaded where it is added.  (Even so 40 to 56 bytes a lane are in scratch: 128 registers, of which
+  // weights and sums keep 48.)
   constexpr bool kAhead = CH == 1;
   const bool joined = gtotal != nullptr && gx != nullptr;
   const float share = 1.0f / (float)n.H;

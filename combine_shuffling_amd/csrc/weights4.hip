@@ -1,7 +1,10 @@
 // Packing, quantizing and unpacking of 4-bit expert weights on gfx950 (the
 // layout is described in block_internal.h).  Weights are laid out once, before
-// serving starts; these kernels are bound by HBM.  A wave takes a tile of 16 rows by
-// 128 along K, a lane the 16 bytes that it has in the layout.
+// serving starts.  A wave takes a tile of 16 rows by 128 along K, a lane the 16 bytes
+// that it has in the layout: whole lines on the packed side, 64 bytes (of codes, 16) of
+// each of 16 rows at a time on the other.  64 x 2048 x 2048 weights, by format, of a
+// copy's 4.7 TB/s: packing 92 to 128 us (2.4 to 3.0 TB/s), quantizing 192 to 224 (3.1 to 3.5),
+// unpacking to bf16 148 to 176 (3.9 to 4.6); groups of 32 take the longest.
 #include <algorithm>
 
 #include "block_internal.h"

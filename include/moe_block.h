@@ -53,8 +53,9 @@ typedef struct moe_norm_config {
  * NULL.  total may be NULL with a residual too (not wanted).  gamma, beta: [H]
  * float32, NULL for ones and zeros.  y: [T, H].  stats: [T, 2] float32, mean
  * and rstd, as the gradient takes them, 8-byte aligned, or NULL.
- * A row whose sum of squares passes float32's range has rstd 0.  The plan need
- * not be routed; its experts take no part.  Limit: H <= 16384.
+ * A row whose sum of squares passes float32's range has rstd 0, and one whose
+ * sum does (layer norm) NaN for y.  The plan need not be routed; its experts
+ * take no part.  Limit: H <= 16384.
  * Errors: INVALID_ARGUMENT (null or misaligned pointers, unknown kind or
  * dtype, eps negative or not finite, a total without a residual), UNSUPPORTED
  * (H beyond the limit), HIP. */
@@ -140,7 +141,7 @@ moe_status moe_weights4_unpack(const moe_weights4_config* cfg, const void* packe
  * rows and in_features are the plan's E and cfg's Z and K.  A row of x with an
  * infinity or a NaN gives a row that is not finite.  INT4 in groups of 32 is for
  * batches of few rows an expert: large ones take two to three times as long as
- * with groups of 64 or 128.
+ * with groups of 64 or 128, and up to seven times where one expert has most rows.
  * Errors: PLAN_NOT_ROUTED, INVALID_ARGUMENT, UNSUPPORTED (sizes beyond the
  * limits), HIP. */
 moe_status moe_expert_linear4(moe_plan* plan, const moe_expert_config* cfg,
